@@ -74,6 +74,17 @@ _SIGS = {
                                ctypes.c_int),
     "gdn_conv_prefill": ([_vp, ctypes.c_int, _vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
                           _vp, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "gdn_attn_append": ([_vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _i32, _i32, _vp, _vp, _vp, _i64, _i32,
+                         _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _vp], ctypes.c_int),
+    "gdn_attn_prefill": ([_vp, _vp, _vp, ctypes.c_int, _vp, _i32, _i64, _i32, _i32, _i32, _i32, _f32, _vp, _vp, _vp,
+                          _sz, _vp], ctypes.c_int),
+    "gdn_attn_prefill_paged": ([_vp, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32, _i32,
+                                _i32, _f32, _vp, _vp, _vp, _sz, _vp], ctypes.c_int),
+    "gdn_attn_prefill_workspace_bytes": ([_i64, _i32, _i32, _i32, _i32, ctypes.c_int], _sz),
+    "gdn_attn_decode": ([_vp, ctypes.c_int, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _f32, _vp,
+                         _vp, _vp, _sz, _vp], ctypes.c_int),
+    "gdn_attn_decode_workspace_bytes": ([_i32, _i32, _i32, _i32, ctypes.c_int], _sz),
+    "gdn_attn_status": ([ctypes.POINTER(_i32)], ctypes.c_int),
     "gdn_decode_step_gated": ([_vp, _vp, _vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _vp, _vp, _vp, _i32, _i32,
                                _i32, _i32, _i32, _f32, _i32, _vp, _vp], ctypes.c_int),
 }
@@ -498,6 +509,188 @@ def gdn_decode_status() -> int:
     st = lib().gdn_decode_status(ctypes.byref(word))
     if st not in (0, 8):
         _check(st, "gdn_decode_status")
+    return int(word.value)
+
+
+# ---------------------------------------------------------------------------
+# The attention layers: a paged key-value cache and the attentions that read it.
+def _same_device(ref: torch.Tensor, *ts):
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"tensors on {ref.device} and {t.device}")
+
+
+def _int32(*ts):
+    for t in ts:
+        if t is not None and t.dtype != torch.int32:
+            raise TypeError("cu_seqlens, kv_lens and block_table must be int32")
+
+
+def _cache_sizes(k_cache, v_cache, block_table, kv_lens, dtype):
+    """(n_pages, page_size, HKV, D, n_seqs, max_pages) of a paged cache, checked."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache, v_cache must be [n_pages, page_size, HKV, D]")
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError("the cache must have the dtype of the new tokens")
+    if block_table.dim() != 2 or kv_lens.shape != (block_table.shape[0],):
+        raise ValueError("block_table must be [n_seqs, max_pages] and kv_lens [n_seqs]")
+    _int32(block_table, kv_lens)
+    return (*k_cache.shape, *block_table.shape)
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    """Elements between the tokens of [tokens, heads, D], heads contiguous within a token."""
+    if not t.is_cuda:
+        raise ValueError("tensors must be CUDA tensors")
+    D = t.shape[2]
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError("a token's heads must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _attn_ws(workspace, need: int, what: str, device):
+    if need == 0:
+        _check(4, what)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def attn_prefill_workspace_bytes(n_tokens, n_seqs, HQ, HKV, D, io_dtype) -> int:
+    return int(lib().gdn_attn_prefill_workspace_bytes(n_tokens, n_seqs, HQ, HKV, D, io_dtype))
+
+
+def attn_decode_workspace_bytes(B, HQ, HKV, D, io_dtype) -> int:
+    return int(lib().gdn_attn_decode_workspace_bytes(B, HQ, HKV, D, io_dtype))
+
+
+def gdn_attn_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=None, inv_freq=None,
+                    interleaved: bool = False, q_out=None):
+    """New tokens into the paged cache: q [T, HQ, D] (or None), k, v [T, HKV, D], views whose
+    tokens are strided (a fused projection's) among them; k_cache, v_cache [n_pages, page_size,
+    HKV, D]; block_table int32 [N, max_pages]; kv_lens int32 [N], the new tokens counted;
+    cu_seqlens int32 [N + 1], or None for one token per sequence; inv_freq fp32
+    [rotary_dim / 2], or None for no rotation.  Returns the rotated queries q_out [T, HQ, D]
+    (None if q is None); q_out may be q."""
+    T, HKV, D = k.shape
+    n_pages, page_size, cHKV, cD, N, max_pages = _cache_sizes(k_cache, v_cache, block_table, kv_lens, k.dtype)
+    if v.shape != k.shape or v.dtype != k.dtype or (cHKV, cD) != (HKV, D):
+        raise ValueError("k, v must be [T, HKV, D] of one dtype, with the cache's HKV and D")
+    HQ = HKV
+    if q is not None:
+        HQ = q.shape[1]
+        if q.shape != (T, HQ, D) or q.dtype != k.dtype:
+            raise ValueError("q must be [T, HQ, D] with the dtype of k")
+        if q_out is None:
+            q_out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError("q_out must be shaped and typed like q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rotary = 0
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+            raise TypeError("inv_freq must be fp32 [rotary_dim / 2]")
+        rotary = 2 * inv_freq.numel()
+    _int32(cu_seqlens)
+    if cu_seqlens is not None and cu_seqlens.shape != (N + 1,):
+        raise ValueError("cu_seqlens must be [n_seqs + 1]")
+    _same_device(k, q, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, inv_freq, q_out)
+    with torch.cuda.device(k.device):
+        st = lib().gdn_attn_append(
+            None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(k),
+            0 if q is None else _token_stride(q), _token_stride(k), _token_stride(v), _ptr(inv_freq), rotary,
+            int(bool(interleaved)), _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), T, N, HQ, HKV, D, n_pages,
+            page_size, max_pages, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _stream())
+    _check(st, "gdn_attn_append")
+    return q_out
+
+
+def _attn_out(q, z, o):
+    if z is not None and (z.shape != q.shape or z.dtype != q.dtype):
+        raise ValueError("z must be shaped and typed like q")
+    if o is None:
+        return torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o must be shaped and typed like q")
+    return o
+
+
+def gdn_attn_prefill(q, k, v, cu_seqlens=None, scale: float | None = None, z=None, o=None, workspace=None):
+    """Causal attention of whole prompts: q [B, T, HQ, D], k, v [B, T, HKV, D] (packed: B = 1
+    and cu_seqlens int32 [N + 1]); scale defaults to 1 / sqrt(D); z like q gates the output by
+    sigmoid(z).  Returns o like q."""
+    B, T, HQ, D = q.shape
+    HKV = k.shape[2]
+    if k.shape != (B, T, HKV, D) or v.shape != k.shape:
+        raise ValueError("inconsistent q/k/v shapes")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise TypeError("q, k, v must share one dtype")
+    _int32(cu_seqlens)
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
+    o = _attn_out(q, z, o)
+    _same_device(q, k, v, cu_seqlens, z, o, workspace)
+    need = attn_prefill_workspace_bytes(B * T, N, HQ, HKV, D, _dtype_code(q))
+    with torch.cuda.device(q.device):
+        workspace, nws = _attn_ws(workspace, need, "gdn_attn_prefill", q.device)
+        st = lib().gdn_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(cu_seqlens), B, T, N, HQ, HKV, D,
+                                    D ** -0.5 if scale is None else float(scale), _ptr(z), _ptr(o), _ptr(workspace),
+                                    nws, _stream())
+    _check(st, "gdn_attn_prefill")
+    return o
+
+
+def gdn_attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, scale: float | None = None, z=None,
+                           o=None, workspace=None):
+    """Prompt pieces over the paged cache that holds their past and themselves: q [T, HQ, D]
+    packed by cu_seqlens int32 [N + 1]; cache, block_table and kv_lens as gdn_attn_append;
+    scale and z as gdn_attn_prefill.  Returns o like q."""
+    T, HQ, D = q.shape
+    n_pages, page_size, HKV, cD, N, max_pages = _cache_sizes(k_cache, v_cache, block_table, kv_lens, q.dtype)
+    if cD != D or cu_seqlens.shape != (N + 1,):
+        raise ValueError("the cache must have q's head dim, and cu_seqlens must be [n_seqs + 1]")
+    _int32(cu_seqlens)
+    o = _attn_out(q, z, o)
+    _same_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, z, o, workspace)
+    need = attn_prefill_workspace_bytes(T, N, HQ, HKV, D, _dtype_code(q))
+    with torch.cuda.device(q.device):
+        workspace, nws = _attn_ws(workspace, need, "gdn_attn_prefill_paged", q.device)
+        st = lib().gdn_attn_prefill_paged(_ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                          _ptr(kv_lens), _ptr(cu_seqlens), T, N, HQ, HKV, D, n_pages, page_size,
+                                          max_pages, D ** -0.5 if scale is None else float(scale), _ptr(z), _ptr(o),
+                                          _ptr(workspace), nws, _stream())
+    _check(st, "gdn_attn_prefill_paged")
+    return o
+
+
+def gdn_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale: float | None = None, z=None, o=None,
+                    workspace=None):
+    """One new token per sequence attends to its pages: q [B, HQ, D]; cache, block_table [B,
+    max_pages] and kv_lens [B] as gdn_attn_append; scale and z as gdn_attn_prefill.  Returns o
+    like q."""
+    B, HQ, D = q.shape
+    n_pages, page_size, HKV, cD, N, max_pages = _cache_sizes(k_cache, v_cache, block_table, kv_lens, q.dtype)
+    if cD != D or N != B:
+        raise ValueError("the cache must have q's head dim, and block_table one row per sequence")
+    o = _attn_out(q, z, o)
+    _same_device(q, k_cache, v_cache, block_table, kv_lens, z, o, workspace)
+    need = attn_decode_workspace_bytes(B, HQ, HKV, D, _dtype_code(q))
+    with torch.cuda.device(q.device):
+        workspace, nws = _attn_ws(workspace, need, "gdn_attn_decode", q.device)
+        st = lib().gdn_attn_decode(_ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                   _ptr(kv_lens), B, HQ, HKV, D, n_pages, page_size, max_pages,
+                                   D ** -0.5 if scale is None else float(scale), _ptr(z), _ptr(o), _ptr(workspace),
+                                   nws, _stream())
+    _check(st, "gdn_attn_decode")
+    return o
+
+
+def gdn_attn_status() -> int:
+    """Synchronise the device, return the attention calls' error word and clear it."""
+    word = _i32(0)
+    st = lib().gdn_attn_status(ctypes.byref(word))
+    if st not in (0, 8):
+        _check(st, "gdn_attn_status")
     return int(word.value)
 
 

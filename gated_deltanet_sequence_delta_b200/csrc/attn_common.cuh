@@ -1,0 +1,82 @@
+// attn_common.cuh -- declarations shared by the attention kernels' .cu files.
+#pragma once
+
+#include "gdn_internal.cuh"
+#include "paged.cuh"
+
+namespace gdn {
+
+// The key-value cache as the kernels see it.  table null: no cache; keys and values are the
+// packed (or dense) tensors k, v, indexed like the queries.
+struct AttnKv {
+    const void* k;              // [n_pages, page_size, HKV, D], or [tokens, HKV, D]
+    const void* v;
+    const int32_t* table;       // [n_seqs, max_pages]
+    const int32_t* kv_lens;     // [n_seqs]
+    int n_pages, page_shift, max_pages;
+};
+
+struct AttnArgs {
+    const void* q;              // [n_tokens, HQ, D]
+    AttnKv kv;
+    const int32_t* cu;          // [n_seqs + 1], or null: T tokens per sequence
+    int64_t T;                  // tokens per sequence (dense)
+    int64_t n_tokens;
+    int n_seqs, HQ, HKV, D;
+    float scale;
+    const void* z;              // output gate inputs [n_tokens, HQ, D], or null
+    void* o;                    // [n_tokens, HQ, D]
+    bool bf16;
+    void* ws;                   // scratch
+};
+
+struct AppendArgs {
+    const void* q;              // may be null (with q_out)
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;   // elements between tokens
+    const float* inv_freq;      // [rotary / 2]
+    int rotary;                 // leading elements of a head that are rotated
+    bool interleaved;
+    const int32_t* cu;
+    int64_t n_tokens;
+    int n_seqs, HQ, HKV, D;
+    void* q_out;
+    void* k_cache;
+    void* v_cache;
+    const int32_t* table;
+    const int32_t* kv_lens;
+    int n_pages, page_shift, max_pages;
+    bool bf16;
+};
+
+__device__ __forceinline__ SeqRows seq_rows(const AttnArgs& a, int n) {
+    return seq_rows(a.cu, a.kv.kv_lens, n, a.T, a.n_tokens, (int64_t)a.kv.max_pages << a.kv.page_shift);
+}
+
+// Scratch of the prompt attentions, built by the plan kernel and filled in by the main one:
+// word 0 the number of tiles, word 1 the number of tiles to redo, then {sequence, tile} pairs
+// (longest key range first), then {sequence, head, first token, 0} records of tiles to redo.
+struct AttnPlan {
+    int32_t* counts;
+    int2* tiles;
+    int4* redo;
+    int max_tiles;
+    size_t bytes;
+};
+// Tiles of `tile_rows` rows, `row_per_tok` rows a token.
+AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int heads, int row_per_tok, int tile_rows);
+cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s);
+
+// out * sigmoid(z)
+__device__ __forceinline__ float gate_out(float o, float z) { return o / (1.0f + expf(-z)); }
+
+cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
+size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
+
+// Read (and clear) the device word each file's kernels set on a bad table or an expired wait.
+cudaError_t read_append_error(int32_t* out);
+cudaError_t read_attn_cudacore_error(int32_t* out);
+
+}  // namespace gdn

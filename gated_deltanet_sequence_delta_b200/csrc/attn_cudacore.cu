@@ -1,0 +1,345 @@
+// attn_cudacore.cu -- causal grouped attention on the CUDA cores, for packed prompts and for
+// the paged cache: the fp32 mode of the prompt calls (no TF32), and the careful second pass
+// over bf16 tiles whose tensor-core result is not finite.
+//
+//   o_i = sum_{j <= p_i} e^{s_ij - m_i} v_j / sum_{j <= p_i} e^{s_ij - m_i},  s_ij = scale q_i.k_j,
+// p_i the position of row i, in one pass over the keys with the running maximum m and sum.
+//
+// The rows of a tile are (token, query head of the group) pairs of one key-value head, so the
+// group shares each key and value that is staged.  64 rows x 64 keys a step, 256 threads, a
+// 4 x 4 block of scores and 4 x D/16 outputs each; row statistics stay within a half-warp.
+// Bound: shared-memory reads (8 16-byte reads per 64 FMAs), about half of the fp32 rate.
+//
+// Masked places never enter a sum, neither their scores nor 0 * v_j, so infinities and NaN in
+// values a row does not see leave it alone.
+#include "attn_common.cuh"
+
+namespace gdn {
+namespace {
+
+__device__ int g_cc_error;
+
+constexpr int kThreads = 256;
+constexpr int kM = 64, kN = 64;
+constexpr int kPStride = kN + 4;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int D>
+struct Smem {
+    float q[kM][D];
+    union {                 // the probabilities take the keys' place once the scores are formed,
+        float k[kN][D + 4]; // so that two blocks fit an SM
+        float p[kM][kPStride];
+    };
+    float v[kN][D];
+    int64_t row[kN];        // row of k, v that holds each key of the step, -1: none
+    int lim[kM];            // last key position each row sees, -1: none
+};
+
+template <typename IO>
+__device__ __forceinline__ float4 load4(const IO* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) {
+    return *reinterpret_cast<const float4*>(p);
+}
+template <>
+__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    const __nv_bfloat162 a = *reinterpret_cast<const __nv_bfloat162*>(&r.x);
+    const __nv_bfloat162 b = *reinterpret_cast<const __nv_bfloat162*>(&r.y);
+    return make_float4(__low2float(a), __high2float(a), __low2float(b), __high2float(b));
+}
+
+// One tile: rows row0 .. row0 + 63 of sequence n's (token, head) rows, row r being token
+// r / per and query head head0 + r % per, against key-value head kvh.
+template <typename IO, int D>
+__device__ void attn_tile(const AttnArgs& a, Smem<D>& sm, const SeqRows& sq, int n, int kvh, int64_t row0, int per,
+                          int head0, int64_t row_end) {
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int past = sq.n_kv - sq.n_q;
+    const IO* q = (const IO*)a.q;
+    const IO* K = (const IO*)a.kv.k;
+    const IO* V = (const IO*)a.kv.v;
+    __syncthreads();                 // the previous tile's reads of shared memory are over
+    for (int i = tid; i < kM; i += kThreads) {
+        const int64_t r = row0 + i;
+        sm.lim[i] = r < row_end ? past + (int)(r / per) : -1;
+    }
+    for (int i = tid; i < kM * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (row0 + r < row_end) {
+            const int64_t tok = sq.q0 + (row0 + r) / per;
+            x = load4(q + (tok * a.HQ + head0 + (int)((row0 + r) % per)) * D + c);
+        }
+        *reinterpret_cast<float4*>(&sm.q[r][c]) = x;
+    }
+    __syncthreads();
+    int lim[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lim[i] = sm.lim[ty * 4 + i];
+    const int64_t last_row = min(row0 + kM, row_end) - 1;
+    const int end = max(past + (int)(last_row / per) + 1, 0);     // keys the tile's last row sees
+    const int lim_lo = row0 + kM <= row_end ? past + (int)(row0 / per) : -1;
+    const float sc = a.scale * kLog2e;
+
+    float o[4][D / 16], m[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+    for (int j0 = 0; j0 < end; j0 += kN) {
+        if (tid < kN) {
+            int64_t row = -1;
+            const int pos = j0 + tid;
+            if (pos < end) {
+                if (a.kv.table) {
+                    row = cache_row(a.kv.table + (int64_t)n * a.kv.max_pages, pos, a.kv.page_shift, a.kv.n_pages);
+                    if (row < 0) atomicMax(&g_cc_error, GDN_DEVERR_PAGE);
+                } else {
+                    row = sq.q0 + pos;
+                }
+            }
+            sm.row[tid] = row;
+        }
+        __syncthreads();
+        for (int i = tid; i < kN * (D / 4); i += kThreads) {
+            const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+            if (sm.row[r] >= 0) {
+                const int64_t at = (sm.row[r] * a.HKV + kvh) * D + c;
+                x = load4(K + at);
+                y = load4(V + at);
+            }
+            *reinterpret_cast<float4*>(&sm.k[r][c]) = x;
+            *reinterpret_cast<float4*>(&sm.v[r][c]) = y;
+        }
+        __syncthreads();
+        float s[4][4] = {};
+#pragma unroll 4
+        for (int d = 0; d < D; d += 4) {
+            float4 qa[4], kb[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qa[i] = *reinterpret_cast<const float4*>(&sm.q[ty * 4 + i][d]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kb[j] = *reinterpret_cast<const float4*>(&sm.k[tx + 16 * j][d]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = fmaf(qa[i].x, kb[j].x, s[i][j]);
+                    s[i][j] = fmaf(qa[i].y, kb[j].y, s[i][j]);
+                    s[i][j] = fmaf(qa[i].z, kb[j].z, s[i][j]);
+                    s[i][j] = fmaf(qa[i].w, kb[j].w, s[i][j]);
+                }
+        }
+        __syncthreads();             // every score is formed: p may overwrite k
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = m[i];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[i][j] = j0 + tx + 16 * j <= lim[i] ? s[i][j] * sc : -INFINITY;
+                mx = fmaxf(mx, s[i][j]);
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+            const float base = mx == -INFINITY ? 0.f : mx;      // a row that has seen no key yet
+            const float alpha = exp2f(m[i] - base);
+            m[i] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float p = j0 + tx + 16 * j <= lim[i] ? exp2f(s[i][j] - base) : 0.f;
+                sm.p[ty * 4 + i][tx + 16 * j] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            l[i] = l[i] * alpha + sum;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) o[i][c] *= alpha;
+        }
+        __syncwarp();                // a row's p is written and read by the same half-warp
+        if (j0 + kN - 1 <= lim_lo) {
+#pragma unroll 2
+            for (int j = 0; j < kN; j += 4) {
+                float4 p[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4*>(&sm.p[ty * 4 + i][j]);
+#pragma unroll
+                for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+                    for (int c = 0; c < D / 64; ++c) {
+                        const float4 v = *reinterpret_cast<const float4*>(&sm.v[j + jj][c * 64 + tx * 4]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float pi = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+                            o[i][c * 4 + 0] = fmaf(pi, v.x, o[i][c * 4 + 0]);
+                            o[i][c * 4 + 1] = fmaf(pi, v.y, o[i][c * 4 + 1]);
+                            o[i][c * 4 + 2] = fmaf(pi, v.z, o[i][c * 4 + 2]);
+                            o[i][c * 4 + 3] = fmaf(pi, v.w, o[i][c * 4 + 3]);
+                        }
+                    }
+            }
+        } else {                     // some row does not see every key of this step
+            const int stop = min(kN, end - j0);
+            for (int j = 0; j < stop; ++j) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const float4 v = *reinterpret_cast<const float4*>(&sm.v[j][c * 64 + tx * 4]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (j0 + j <= lim[i]) {
+                            const float pi = sm.p[ty * 4 + i][j];
+                            o[i][c * 4 + 0] = fmaf(pi, v.x, o[i][c * 4 + 0]);
+                            o[i][c * 4 + 1] = fmaf(pi, v.y, o[i][c * 4 + 1]);
+                            o[i][c * 4 + 2] = fmaf(pi, v.z, o[i][c * 4 + 2]);
+                            o[i][c * 4 + 3] = fmaf(pi, v.w, o[i][c * 4 + 3]);
+                        }
+                }
+            }
+        }
+        __syncthreads();             // before the next step overwrites k, v
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t r = row0 + ty * 4 + i;
+        if (r >= row_end) continue;
+        const int64_t at = ((sq.q0 + r / per) * a.HQ + head0 + (int)(r % per)) * D;
+        const bool empty = lim[i] < 0;                 // no key: zero
+        const float inv = empty ? 0.f : 1.0f / l[i];
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+            const int64_t e = at + (c >> 2) * 64 + tx * 4 + (c & 3);
+            float x = empty ? 0.f : o[i][c] * inv;
+            if (a.z && !empty) x = gate_out(x, load_elem((const IO*)a.z, e));
+            store_elem((IO*)a.o, e, x);
+        }
+    }
+}
+
+template <typename IO, int D>
+__global__ void __launch_bounds__(kThreads) attn_cc_kernel(AttnArgs a, AttnPlan plan) {
+    extern __shared__ float4 smem_raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+    if ((int)blockIdx.x >= plan.counts[0]) return;
+    const int2 it = plan.tiles[blockIdx.x];
+    const SeqRows sq = seq_rows(a, it.x);
+    const int G = a.HQ / a.HKV;
+    attn_tile<IO, D>(a, sm, sq, it.x, blockIdx.y, (int64_t)it.y * kM, G, blockIdx.y * G, (int64_t)sq.n_q * G);
+}
+
+// The plan: every sequence's tiles, the longest key ranges first (the grid starts them in
+// order, so the short ones fill the end).  Counting sort over kBuckets lengths; the order
+// inside a bucket varies and changes no result.
+constexpr int kPlanThreads = 1024, kBuckets = 256;
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, AttnPlan plan, int per, int tile_rows) {
+    __shared__ int s_count[kBuckets];
+    __shared__ int s_max;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < kBuckets; i += kPlanThreads) s_count[i] = 0;
+    if (tid == 0) s_max = 1;
+    __syncthreads();
+    int mx = 1;
+    for (int n = tid; n < a.n_seqs; n += kPlanThreads) {
+        const SeqRows r = seq_rows(a, n);
+        if (r.bad) atomicMax(&g_cc_error, r.bad);
+        mx = max(mx, r.n_kv);
+    }
+    atomicMax(&s_max, mx);
+    __syncthreads();
+    const int width = (s_max - 1) / kBuckets + 1;
+    auto bucket = [&](const SeqRows& r, int t) {
+        const int64_t last = min(((int64_t)t + 1) * tile_rows, (int64_t)r.n_q * per) - 1;
+        const int keys = max(r.n_kv - r.n_q + (int)(last / per), 0);
+        return kBuckets - 1 - min(keys / width, kBuckets - 1);
+    };
+    // a sequence per warp, a tile per lane
+    for (int pass = 0; pass < 2; ++pass) {
+        for (int n = tid >> 5; n < a.n_seqs; n += kPlanThreads / 32) {
+            const SeqRows r = seq_rows(a, n);
+            const int tiles = (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
+            for (int t = tid & 31; t < tiles; t += 32) {
+                const int at = atomicAdd(&s_count[bucket(r, t)], 1);
+                // sequences of a bad table may overlap: never past the list's end
+                if (pass == 1 && at < plan.max_tiles) plan.tiles[at] = make_int2(n, t);
+            }
+        }
+        __syncthreads();
+        if (pass == 0 && tid == 0) {
+            int sum = 0;
+            for (int i = 0; i < kBuckets; ++i) {
+                const int c = s_count[i];
+                s_count[i] = sum;
+                sum += c;
+            }
+            plan.counts[0] = min(sum, plan.max_tiles);
+            plan.counts[1] = 0;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename IO, int D>
+cudaError_t launch_cc(const AttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
+    cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<IO, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)sizeof(Smem<D>));
+    if (e != cudaSuccess) return e;
+    attn_cc_kernel<IO, D><<<dim3((unsigned)plan.max_tiles, (unsigned)a.HKV), kThreads, sizeof(Smem<D>), s>>>(a, plan);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+}  // namespace
+
+AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int heads, int row_per_tok, int tile_rows) {
+    AttnPlan p;
+    const int64_t tiles = (n_tokens * row_per_tok + tile_rows - 1) / tile_rows + n_seqs;
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    p.max_tiles = (int)tiles;
+    p.counts = reinterpret_cast<int32_t*>(b);
+    size_t at = kStatusBytes;
+    p.tiles = reinterpret_cast<int2*>(b + at);
+    at += (size_t)((tiles * sizeof(int2) + 255) / 256 * 256);
+    p.redo = reinterpret_cast<int4*>(b + at);
+    at += (size_t)(((size_t)tiles * heads * sizeof(int4) + 255) / 256 * 256);
+    p.bytes = at;
+    return p;
+}
+
+cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s) {
+    attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, p, row_per_tok, tile_rows);
+    const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV) {
+    return attn_plan(nullptr, n_tokens, n_seqs, 0, HQ / HKV, kM).bytes;
+}
+
+cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s) {
+    if (a.n_tokens == 0 || a.n_seqs == 0) return cudaSuccess;
+    const int G = a.HQ / a.HKV;
+    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 0, G, kM);
+    cudaError_t e = launch_attn_plan(a, plan, G, kM, s);
+    if (e != cudaSuccess) return e;
+    if (a.bf16) return a.D == 128 ? launch_cc<__nv_bfloat16, 128>(a, plan, s) : launch_cc<__nv_bfloat16, 64>(a, plan, s);
+    return a.D == 128 ? launch_cc<float, 128>(a, plan, s) : launch_cc<float, 64>(a, plan, s);
+}
+
+cudaError_t read_attn_cudacore_error(int32_t* out) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_cc_error, sizeof(int32_t));
+    if (e == cudaSuccess && *out != 0) {
+        const int32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_cc_error, &zero, sizeof(int32_t));
+    }
+    return e;
+}
+
+}  // namespace gdn

@@ -4,8 +4,17 @@
 
 #include <atomic>
 
+#include "api_checks.cuh"
 #include "gdn.h"
 #include "gdn_internal.cuh"
+
+using gdn::aligned16;
+using gdn::cuda_status;
+using gdn::dtype_ok;
+using gdn::esize;
+using gdn::head_dim_ok;
+using gdn::overlap;
+using gdn::Range;
 
 namespace {
 
@@ -13,32 +22,14 @@ thread_local int g_last_cuda_error = 0;
 std::atomic<uint64_t> g_launches{0};
 std::atomic<int> g_stall_site{0};   // gdn_testing_stall
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-struct Range {
-    const void* p;
-    size_t bytes;
-};
-
-bool overlap(Range a, Range b) {
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-size_t esize(gdn_dtype d) { return d == GDN_BF16 ? 2 : 4; }
-bool dtype_ok(gdn_dtype d) { return d == GDN_F32 || d == GDN_BF16; }
-bool head_dim_ok(int32_t d) { return d == 64 || d == 128; }
-
+namespace gdn {
 gdn_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return GDN_OK;
     g_last_cuda_error = (int)e;
     return GDN_ERR_CUDA;
 }
-
-}  // namespace
-
-namespace gdn {
 void count_launch(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 int testing_stall_site() { return g_stall_site.load(std::memory_order_relaxed); }
 }  // namespace gdn

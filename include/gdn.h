@@ -65,6 +65,7 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 #define GDN_DEVERR_NONE 0
 #define GDN_DEVERR_CU_SEQLENS 1   /* cu_seqlens[0] != 0, decreasing, or last != T */
 #define GDN_DEVERR_TIMEOUT 2      /* a bounded wait inside a kernel expired; outputs invalid */
+#define GDN_DEVERR_PAGE 3         /* a block-table entry or context length is out of range */
 
 /* Human-readable name of a gdn_status value (static storage, never NULL). */
 GDN_API const char* gdn_status_string(int status);
@@ -475,6 +476,125 @@ GDN_API gdn_status gdn_decode_step_fused_outgate(const void* x, gdn_dtype io_dty
  * NULL argument, CUDA on a CUDA error.
  */
 GDN_API gdn_status gdn_decode_status(int32_t* device_error);
+
+/*
+ * The attention layers of the hybrid stack: in the 3:1 layout of the "Gated DeltaNet / Qwen 3.5
+ * tutorial" page (section 6) every fourth layer is gated full attention with grouped heads,
+ * over the same packed batch as the gated delta rule beside it.  Four calls:
+ *   gdn_attn_append         new tokens' keys and values into a paged cache, rotated by position
+ *   gdn_attn_decode         one new token per sequence attends to its pages
+ *   gdn_attn_prefill        whole prompts, keys and values packed like the queries
+ *   gdn_attn_prefill_paged  pieces of prompts attend to the pages that hold their past and them
+ * Per query head h (key-value head h / (HQ / HKV)) and token i at position p_i of its sequence:
+ *     o_i = sum_{j <= p_i} w_ij v_j / sum_{j <= p_i} w_ij,   w_ij = exp(scale q_i . k_j),
+ * and with z given, o_i * sigmoid(z_i) per element (the output gate of the GDN resource-
+ * allocation page).  A token that sees no key gets zeros.  Places a token does not see never
+ * enter its sums, whatever they hold (infinities, NaN).
+ *
+ * Shared by the four calls:
+ *   k_cache, v_cache [n_pages, page_size, HKV, D] io_dtype; page_size 16, 32, 64 or 128
+ *   block_table [n_seqs, max_pages] int32: page block_table[n][p / page_size] holds position p
+ *               of sequence n at offset p % page_size.  Entries past a sequence's context are
+ *               not read.  Sequences may share pages that a call only reads.
+ *   kv_lens     [n_seqs] int32: tokens in each sequence's context, the call's own new tokens
+ *               among them.  New token i of n_new has position kv_lens - n_new + i; a token
+ *               whose position is negative (kv_lens = 0: an idle slot of a padded batch) is
+ *               not appended and sees no key.
+ *   cu_seqlens  [n_seqs + 1] int32: new tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1 belong to
+ *               sequence n.  Rows from cu_seqlens[n_seqs] on are left as they were.
+ *   D 64 or 128, HQ % HKV == 0, at most 1024 heads.
+ * The tables are checked on the device, where they live: a sequence whose cu_seqlens or kv_lens
+ * entries are out of range is skipped (its outputs are left as they were), a page number out of
+ * range is never followed (what would have been written there is dropped; a sequence that reads
+ * it gets undefined outputs); other sequences are not affected.  The first such finding is kept
+ * in a device word that gdn_attn_status reads.
+ */
+
+/*
+ * gdn_attn_append -- the new tokens of each sequence enter the cache.  The first rotary_dim
+ * elements of each query and key head turn by their position p: pair i (elements i and
+ * i + rotary_dim / 2; with `interleaved`, 2 i and 2 i + 1) by the angle p * inv_freq[i],
+ *     (a, b) -> (a cos - b sin, b cos + a sin),
+ * the angle exact to float rounding at every position.  Then k and v go to their pages and q to
+ * q_out.
+ *   q        [n_tokens, HQ, D], k, v [n_tokens, HKV, D] io_dtype, q_stride, k_stride, v_stride
+ *            elements from token to token, so that views of a fused projection can be passed
+ *            (heads contiguous within a token; strides multiples of 16 bytes)        (read)
+ *   inv_freq [rotary_dim / 2] fp32, radians per position (may be NULL if rotary_dim is 0) (read)
+ *   rotary_dim  0 (no rotation) to D, a multiple of 16
+ *   cu_seqlens  or NULL: one token per sequence (n_tokens == n_seqs, a decode step)  (read)
+ *   q_out    [n_tokens, HQ, D] io_dtype, may be q itself where q_stride is HQ * D; q and q_out
+ *            both NULL: keys and values only                                        (written)
+ *   k_cache, v_cache   the new tokens' slots only                                    (written)
+ * Tokens that are not appended leave their q_out row as it was.  No two tokens of a call may
+ * name the same slot.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, ALIAS, CUDA.
+ */
+GDN_API gdn_status gdn_attn_append(const void* q, const void* k, const void* v, gdn_dtype io_dtype,
+                                   int64_t q_stride, int64_t k_stride, int64_t v_stride, const float* inv_freq,
+                                   int32_t rotary_dim, int32_t interleaved, const int32_t* cu_seqlens,
+                                   const int32_t* kv_lens, const int32_t* block_table, int64_t n_tokens,
+                                   int32_t n_seqs, int32_t HQ, int32_t HKV, int32_t D, int32_t n_pages,
+                                   int32_t page_size, int32_t max_pages, void* q_out, void* k_cache, void* v_cache,
+                                   void* stream);
+
+/*
+ * gdn_attn_prefill -- causal attention of whole prompts to themselves.
+ *   q        [B, T, HQ, D], k, v [B, T, HKV, D] io_dtype                        (read)
+ *   cu_seqlens  NULL: B sequences of T tokens, n_seqs == B; else packed, B == 1   (read)
+ *   z        [B, T, HQ, D] io_dtype, or NULL: no output gate                    (read)
+ *   o        [B, T, HQ, D] io_dtype                                             (written)
+ *   scale    multiplies the scores (1 / sqrt(D) in the usual reading); finite
+ *   workspace   device scratch of >= gdn_attn_prefill_workspace_bytes(...) bytes; contents need
+ *            not be initialised; not shared by calls that may run concurrently
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, ALIAS, WORKSPACE, CUDA.
+ */
+GDN_API gdn_status gdn_attn_prefill(const void* q, const void* k, const void* v, gdn_dtype io_dtype,
+                                    const int32_t* cu_seqlens, int32_t B, int64_t T, int32_t n_seqs, int32_t HQ,
+                                    int32_t HKV, int32_t D, float scale, const void* z, void* o, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * gdn_attn_prefill_paged -- each sequence's new tokens attend to its pages, which hold their past
+ * and themselves (gdn_attn_append first): prompts taken in pieces, drafts to be verified.
+ *   q, z, o  [n_tokens, HQ, D] io_dtype, packed by cu_seqlens; z may be NULL
+ *   the rest as above and in gdn_attn_prefill, whose workspace size applies.
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, ALIAS, WORKSPACE, CUDA.
+ */
+GDN_API gdn_status gdn_attn_prefill_paged(const void* q, gdn_dtype io_dtype, const void* k_cache,
+                                          const void* v_cache, const int32_t* block_table, const int32_t* kv_lens,
+                                          const int32_t* cu_seqlens, int64_t n_tokens, int32_t n_seqs, int32_t HQ,
+                                          int32_t HKV, int32_t D, int32_t n_pages, int32_t page_size,
+                                          int32_t max_pages, float scale, const void* z, void* o, void* workspace,
+                                          size_t workspace_bytes, void* stream);
+
+/* Workspace of gdn_attn_prefill (n_tokens = B * T) and gdn_attn_prefill_paged; 0 for sizes that
+ * they would reject. */
+GDN_API size_t gdn_attn_prefill_workspace_bytes(int64_t n_tokens, int32_t n_seqs, int32_t HQ, int32_t HKV, int32_t D,
+                                                gdn_dtype io_dtype);
+
+/*
+ * gdn_attn_decode -- one new token per sequence attends to its pages (gdn_attn_append first), the
+ * attention layers' counterpart of gdn_decode_step.
+ *   q, z, o  [B, HQ, D] io_dtype; z may be NULL; the rest as above (n_seqs = B).
+ * B may be 0 (nothing launched).
+ * Errors: NULL, SHAPE, ALIGN, UNSUPPORTED, ALIAS, WORKSPACE, CUDA.
+ */
+GDN_API gdn_status gdn_attn_decode(const void* q, gdn_dtype io_dtype, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_table, const int32_t* kv_lens, int32_t B, int32_t HQ,
+                                   int32_t HKV, int32_t D, int32_t n_pages, int32_t page_size, int32_t max_pages,
+                                   float scale, const void* z, void* o, void* workspace, size_t workspace_bytes,
+                                   void* stream);
+
+/* Workspace of gdn_attn_decode; 0 for sizes that it would reject. */
+GDN_API size_t gdn_attn_decode_workspace_bytes(int32_t B, int32_t HQ, int32_t HKV, int32_t D, gdn_dtype io_dtype);
+
+/*
+ * Synchronises the device, then reads and clears the device word of the attention calls
+ * (GDN_DEVERR_NONE, _CU_SEQLENS, _TIMEOUT or _PAGE, shared by every such call on that device)
+ * into *device_error.  Returns GDN_ERR_DEVICE if it is nonzero.  Errors: NULL, CUDA.
+ */
+GDN_API gdn_status gdn_attn_status(int32_t* device_error);
 
 /*
  * gdn_testing_stall -- a test hook with no counterpart in the method: it lets a test see
