@@ -83,7 +83,7 @@ size_t prefill_bytes(int64_t n_tokens, int32_t n_seqs, int32_t HQ, int32_t HKV, 
 
 size_t decode_bytes(int32_t B, int32_t HQ, int32_t HKV, int32_t D, gdn_dtype io) {
     if (B < 0 || check_heads(io, HQ, HKV, D) != GDN_OK) return 0;
-    return gdn::attn_cudacore_bytes(B, B, HQ, HKV);
+    return gdn::attn_decode_bytes(D);
 }
 
 }  // namespace
@@ -194,7 +194,7 @@ gdn_status gdn_attn_decode(const void* q, gdn_dtype io_dtype, const void* k_cach
                      nullptr, 1, B, B, HQ, HKV, D, scale, z, o, io_dtype == GDN_BF16, workspace};
     st = check_attn(a, io_dtype, decode_bytes(B, HQ, HKV, D, io_dtype), workspace, workspace_bytes);
     if (st != GDN_OK) return st;
-    return cuda_status(gdn::launch_attn_cudacore(a, (cudaStream_t)stream));
+    return cuda_status(gdn::launch_attn_decode(a, (cudaStream_t)stream));
 }
 
 gdn_status gdn_attn_status(int32_t* device_error) {
@@ -202,7 +202,7 @@ gdn_status gdn_attn_status(int32_t* device_error) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_status(e);
     int32_t word = 0;
-    for (auto read : {gdn::read_append_error, gdn::read_attn_cudacore_error}) {
+    for (auto read : {gdn::read_append_error, gdn::read_attn_cudacore_error, gdn::read_attn_decode_error}) {
         int32_t w = 0;
         e = read(&w);
         if (e != cudaSuccess) return cuda_status(e);

@@ -73,10 +73,13 @@ __device__ __forceinline__ float gate_out(float o, float z) { return o / (1.0f +
 
 cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
+size_t attn_decode_bytes(int D);
 size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
 
 // Read (and clear) the device word each file's kernels set on a bad table or an expired wait.
 cudaError_t read_append_error(int32_t* out);
 cudaError_t read_attn_cudacore_error(int32_t* out);
+cudaError_t read_attn_decode_error(int32_t* out);
 
 }  // namespace gdn

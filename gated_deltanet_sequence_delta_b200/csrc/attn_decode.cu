@@ -1,0 +1,716 @@
+// attn_decode.cu -- one new token per sequence attends to its pages of the key-value cache.
+//
+//   o_h = sum_j w_j v_j / sum_j w_j,   w_j = e^{scale q_h . k_j - m},  j over the context.
+//
+// Bound: HBM.  Every key and value is read once for the whole group of query heads that share
+// it; two FLOPs per byte and query head, so even a group of 16 leaves the arithmetic far below
+// the tensor cores' reach.  What decides the time is how many bytes each SM keeps in flight and
+// how evenly the contexts, which are ragged, spread over the SMs.
+//
+// Split.  The work is one list of tiles of KT keys: sequence by sequence, key-value head by
+// head, tile by tile.  The grid is one block per SM; block c takes the tiles from c N / grid to
+// (c + 1) N / grid, so every block reads the same number of bytes whatever the lengths are.  A
+// block's range may begin and end inside a (sequence, head) item; those pieces leave their
+// running maximum, sum and unnormalised output in the workspace, two slots a block, and a second
+// small kernel joins them in the order of the blocks (the result does not depend on timing).
+// Lengths live on the device: each block finds its range by a scan over them.
+//
+// Block: a producer warp copies tiles into a ring in shared memory by TMA, 128B-swizzled, one
+// box per page part (rows of a token's head are 128 or 256 bytes, heads and tokens strided);
+// eight consumer warps in two teams take alternate tiles, a warp a fixed share of a tile's
+// keys, each with its own running statistics, so that teams only meet at the end of an item.
+//   bf16: mma.sync m16n8k16 with the group's heads as M (up to 16), the fragments read by
+//     ldmatrix; tcgen05 would need 128 rows and has nothing to gain on a tile read once.
+//   fp32: CUDA cores (no TF32), a lane a quarter of a key's elements for the scores, D / 32
+//     output columns a lane for the values.
+#include "attn_common.cuh"
+#include "tc_ptx.cuh"
+
+namespace gdn {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+__device__ int g_decode_attn_error;
+
+constexpr int kTeamWarps = 4, kConsumers = 8 * 32, kThreads = kConsumers + 32;
+constexpr int kMaxGrid = 192;             // blocks, for the workspace size
+constexpr float kLog2e = 1.4426950408889634f;
+
+// R: query heads a block serves at once (rows of the statistics).
+template <typename IO, int D, int R>
+struct Cfg {
+    static constexpr int KT = sizeof(IO) == 2 ? 64 : 32;            // keys per tile
+    static constexpr int KW = KT / kTeamWarps;                      // keys per warp: 16 or 8
+    static constexpr int NB = D * (int)sizeof(IO) / 128;            // 128-byte column blocks
+    static constexpr int kBlk = KT * 128;                           // bytes of one column block
+    static constexpr int kStage = 2 * NB * kBlk;                    // keys, then values
+    static constexpr int kMerge = 8 * R * (D + 4) * 4;              // the warps' outputs at an item's end
+    static constexpr int kQ = sizeof(IO) == 4 ? R * D * 4 : 0;      // fp32: the rows' queries
+    static constexpr int kFit = (226 * 1024 - 1024 - kMerge - kQ) / kStage;
+    // ring slots, an even number: a slot then always belongs to the same team, which waits for
+    // every phase of its barrier
+    static constexpr int kStages = kFit > 12 ? 12 : kFit / 2 * 2;
+    static constexpr int kSmem = kStages * kStage + kMerge + kQ + 1024;
+};
+
+__device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, int kt, int* bad) {
+    const SeqRows r = seq_rows(a, n);
+    if (r.bad) *bad = r.bad;
+    return (r.n_kv + kt - 1) / kt;
+}
+
+// Block-wide: the total of per(n) over all sequences, and the sequence that holds unit `at` of
+// the concatenation with the units before it (n = -1: `at` is past the end).
+struct Place {
+    int64_t total, before;
+    int n;
+};
+template <typename F>
+__device__ Place find_place(int n_seqs, F per, int64_t num, int64_t den, int64_t* at, int64_t* s_warp, Place* s_out) {
+    // thread t owns the sequences [t c, (t + 1) c)
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nw = blockDim.x >> 5;
+    const int c = (n_seqs + blockDim.x - 1) / blockDim.x;
+    const int lo = min(tid * c, n_seqs), hi = min(lo + c, n_seqs);
+    int64_t sum = 0;
+    for (int n = lo; n < hi; ++n) sum += per(n);
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    if (lane == 31) s_warp[w] = incl;
+    if (tid == 0) s_out->n = -1;
+    __syncthreads();
+    int64_t base = 0, total = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i < w) base += s_warp[i];
+        total += s_warp[i];
+    }
+    *at = total * num / den;
+    int64_t before = base + incl - sum;
+    if (*at >= before && *at < before + sum) {
+        for (int n = lo; n < hi; ++n) {
+            const int64_t k = per(n);
+            if (*at < before + k) {
+                s_out->n = n;
+                s_out->before = before;
+                break;
+            }
+            before += k;
+        }
+    }
+    __syncthreads();
+    Place p = *s_out;
+    p.total = total;
+    return p;
+}
+
+struct Partials {
+    float* o;             // [grid][2][R][D]
+    float2* ml;           // [grid][2][R]  (m in log2 units, l)
+};
+__host__ __device__ inline Partials partials(void* ws, int R, int D) {
+    Partials p;
+    p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+    p.o = reinterpret_cast<float*>(p.ml + kMaxGrid * 2 * R);
+    return p;
+}
+
+// ---- a warp's running state over the keys it takes ----------------------------------------
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+
+template <typename IO, int D, int R>
+struct Warp;
+
+// bf16: rows are heads, 16 of them; a thread holds rows lane / 4 and lane / 4 + 8.
+template <int D>
+struct Warp<bf16, D, 16> {
+    using C = Cfg<bf16, D, 16>;
+    uint32_t q[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+
+    __device__ __forceinline__ void start(const bf16* qrow, int rows, const float*) {
+        const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const bf16* p = qrow + k * 16 + c;
+            auto at = [&](int row, int col) {
+                return row < rows ? *reinterpret_cast<const uint32_t*>(p + (int64_t)row * D + col) : 0u;
+            };
+            q[k][0] = at(r, 0);
+            q[k][1] = at(r + 8, 0);
+            q[k][2] = at(r, 8);
+            q[k][3] = at(r + 8, 8);
+        }
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+        m[0] = m[1] = -INFINITY;
+        l[0] = l[1] = 0.f;
+    }
+
+    // the warp's 16 keys, rows 16 w .. of the tile, of which the first `valid` exist (> 0)
+    __device__ __forceinline__ void step(uint8_t* tile, int w, int valid, int, float sc, const float*) {
+        const int lane = threadIdx.x & 31;
+        uint8_t* vt = tile + C::NB * C::kBlk;
+        if (valid < 16) {       // values past the context may be anything: 0 * NaN must not enter
+            for (int i = lane; i < (16 - valid) * C::NB * 8; i += 32) {
+                const int row = 16 * w + valid + i / (C::NB * 8), c = i % (C::NB * 8);
+                *reinterpret_cast<uint4*>(vt + (c >> 3) * C::kBlk + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();        // before the ring slot's next copy overwrites them
+            __syncwarp();
+        }
+        const uint32_t kb = tc::smem_u32(tile), vb = tc::smem_u32(vt);
+        const int mat = lane >> 3, mr = lane & 7;
+        float s[2][4] = {};
+        {   // matrices: keys 0-7 and 8-15 (mat >> 1), element halves (mat & 1)
+            const int row = 16 * w + ((mat >> 1) << 3) + mr;
+            const uint32_t base = kb + row * 128;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                uint32_t b[4];
+                const int chunk = (k & 3) * 2 + (mat & 1);
+                ldsm4(base + (k >> 2) * C::kBlk + ((chunk ^ (row & 7)) << 4), b);
+                mma16816(s[0], q[k], b[0], b[1]);
+                mma16816(s[1], q[k], b[2], b[3]);
+            }
+        }
+        float mx[2] = {m[0], m[1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = j * 8 + (lane & 3) * 2 + (i & 1);
+                s[j][i] = key < valid ? s[j][i] * sc : -INFINITY;
+                mx[i >> 1] = fmaxf(mx[i >> 1], s[j][i]);
+            }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
+            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
+        }
+        if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
+            float al[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                al[r] = mx[r] == -INFINITY ? 1.f : exp2f(m[r] - mx[r]);
+                m[r] = mx[r];
+                l[r] *= al[r];
+            }
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j) {
+                o[j][0] *= al[0];
+                o[j][1] *= al[0];
+                o[j][2] *= al[1];
+                o[j][3] *= al[1];
+            }
+        }
+        const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s[j][i] = exp2f(s[j][i] - base[i >> 1]);
+                l[i >> 1] += s[j][i];
+            }
+        // the weights are rounded to bf16 for the product (half a step, 2^-8, each); their sum is not
+        const uint32_t p[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
+                               pack_bf16(s[1][2], s[1][3])};
+        {   // matrices: keys 0-7 and 8-15 (mat & 1), column eights (mat >> 1)
+            const int row = 16 * w + ((mat & 1) << 3) + mr;
+            const uint32_t base_v = vb + row * 128;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                uint32_t b[4];
+                const int chunk = (c & 3) * 2 + (mat >> 1);
+                ldsm4t(base_v + (c >> 2) * C::kBlk + ((chunk ^ (row & 7)) << 4), b);
+                mma16816(o[2 * c], p, b[0], b[1]);
+                mma16816(o[2 * c + 1], p, b[2], b[3]);
+            }
+        }
+    }
+
+    // to shared memory: o rows of D + 4 floats, (m, l) after the columns
+    __device__ __forceinline__ void put(float* out, int rows) {
+        const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+            const int row = r + 8 * h;
+            if (row < rows) {
+                float* p = out + row * (D + 4);
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j)
+                    *reinterpret_cast<float2*>(p + j * 8 + c) = make_float2(o[j][2 * h], o[j][2 * h + 1]);
+                if ((lane & 3) == 0) *reinterpret_cast<float2*>(p + D) = make_float2(m[h], l[h]);
+            }
+        }
+    }
+};
+
+// fp32: a lane holds D / 32 columns of every row's output; the scores of key lane / 4 are
+// summed by its four lanes.
+template <int D, int R>
+struct Warp<float, D, R> {
+    using C = Cfg<float, D, R>;
+    static constexpr int E = D / 32;
+    float o[R][E];
+    float m[R], l[R];      // the same on every lane
+
+    __device__ __forceinline__ void start(const float*, int, const float*) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            m[r] = -INFINITY;
+            l[r] = 0.f;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[r][e] = 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void step(uint8_t* tile, int w, int valid, int rows, float sc, const float* sq) {
+        const int lane = threadIdx.x & 31, key = lane >> 2, part = lane & 3;
+        const uint8_t* vt = tile + C::NB * C::kBlk;
+        const int row = 8 * w + key;
+        float s[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) s[r] = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+            const int c = part + 4 * i;                       // 16-byte chunk of the row
+            const float4 k = *reinterpret_cast<const float4*>(tile + (c >> 3) * C::kBlk + row * 128 +
+                                                              (((c & 7) ^ (row & 7)) << 4));
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float4 q = *reinterpret_cast<const float4*>(sq + r * D + 4 * c);
+                s[r] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, s[r]))));
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
+            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
+            s[r] = key < valid ? s[r] * sc : -INFINITY;
+            float mx = s[r];
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            mx = fmaxf(mx, m[r]);
+            const float base = mx == -INFINITY ? 0.f : mx;
+            const float al = exp2f(m[r] - base);
+            m[r] = mx;
+            s[r] = exp2f(s[r] - base);
+            float sum = s[r];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+            l[r] = fmaf(l[r], al, sum);
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[r][e] *= al;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j < valid) {                   // values past the context never enter
+                const int vr = 8 * w + j;
+                float v[E];
+                const int c = lane * E / 4;    // this lane's columns: E consecutive floats
+                const uint8_t* p = vt + (c >> 3) * C::kBlk + vr * 128 + (((c & 7) ^ (vr & 7)) << 4);
+                if constexpr (E == 4) {
+                    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+                } else {
+                    *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p + (lane & 1) * 8);
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float pr = __shfl_sync(0xffffffffu, s[r], j * 4);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[r][e] = fmaf(pr, v[e], o[r][e]);
+                }
+            }
+        }
+    }
+
+    __device__ __forceinline__ void put(float* out, int rows) {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (r < rows) {
+                float* p = out + r * (D + 4);
+#pragma unroll
+                for (int e = 0; e < E; ++e) p[lane * E + e] = o[r][e];
+                if (lane == 0) *reinterpret_cast<float2*>(p + D) = make_float2(m[r], l[r]);
+            }
+    }
+};
+
+// Where a block is in its range: sequence, (head, row block) of it, tile of that item.
+struct Cursor {
+    int n, sub, tile, tiles, len;
+};
+__device__ __forceinline__ void cursor_load(const AttnArgs& a, Cursor& c, int kt) {
+    while (true) {      // the range ends before the sequences do, so one with tiles exists
+        const SeqRows r = seq_rows(a, c.n);
+        c.len = r.n_kv;
+        c.tiles = (r.n_kv + kt - 1) / kt;
+        if (c.tiles > 0 || c.n + 1 >= a.n_seqs) return;
+        ++c.n;
+    }
+}
+__device__ __forceinline__ void cursor_next(const AttnArgs& a, Cursor& c, int kt, int subs, int64_t left) {
+    if (++c.tile < c.tiles) return;
+    c.tile = 0;
+    if (++c.sub < subs) return;
+    c.sub = 0;
+    if (left > 0 && c.n + 1 < a.n_seqs) {
+        ++c.n;
+        cursor_load(a, c, kt);
+    }
+}
+
+template <typename IO, int D, int R>
+__global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_constant__ CUtensorMap tk,
+                                                                  const __grid_constant__ CUtensorMap tv, AttnArgs a,
+                                                                  int hb) {
+    using C = Cfg<IO, D, R>;
+    constexpr int S = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t s_warp[kThreads / 32];
+    __shared__ Place s_place;
+    __shared__ __align__(8) uint64_t full[S], empty[S];
+    __shared__ int s_dead;
+    // ring tiles 1024-byte aligned (the swizzle's period)
+    uint8_t* ring = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
+    float* merge = reinterpret_cast<float*>(ring + S * C::kStage);
+    float* sq = merge + C::kMerge / 4;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = a.HQ / a.HKV, subs = a.HKV * hb;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], kTeamWarps);
+        }
+        tc::fence_mbar_init();
+        s_dead = 0;
+    }
+    tc::grid_dependency_sync();
+    int bad = 0;
+    int64_t begin;
+    const Place pl = find_place(
+        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, C::KT, &bad) * subs; }, blockIdx.x, gridDim.x, &begin,
+        s_warp, &s_place);
+    if (bad && blockIdx.x == 0) atomicMax(&g_decode_attn_error, bad);
+    const int64_t end = pl.total * (blockIdx.x + 1) / gridDim.x;
+    const int64_t count = end - begin;
+    // contexts of no keys: zeros, a sequence's rows by one block
+    for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
+        const SeqRows r = seq_rows(a, n);
+        if (!r.bad && r.n_kv == 0)
+            for (int i = tid; i < a.HQ * D; i += kThreads) store_elem((IO*)a.o, (int64_t)n * a.HQ * D + i, 0.f);
+    }
+    if (count <= 0) return;
+
+    Cursor cur;
+    cur.n = pl.n;
+    cursor_load(a, cur, C::KT);
+    {
+        const int64_t in_seq = begin - pl.before;
+        cur.sub = (int)(in_seq / cur.tiles);
+        cur.tile = (int)(in_seq - (int64_t)cur.sub * cur.tiles);
+    }
+    const int rows_box = min(1 << a.kv.page_shift, C::KT);
+
+    if (warp == kConsumers / 32) {
+        // ---- producer: lane (g, kind, block) issues one box of the tile
+        const int boxes = C::KT / rows_box;
+        const int lg = lane / (2 * C::NB), lk = (lane / C::NB) & 1, lb = lane % C::NB;
+        const int64_t none = (int64_t)a.kv.n_pages << a.kv.page_shift;        // a row past the cache: zero fill
+        int ent = 0, ent_n = -1, ent_base = 0;      // 32 table entries, one a lane
+        bool ok = true;
+        for (int64_t it = 0; it < count; ++it) {
+            const int st = (int)(it % S);
+            const uint32_t ph = (uint32_t)((it / S) & 1);
+            if (it >= S && ok) {
+                ok = tc::mbar_wait(&empty[st], ph ^ 1);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+            if (!ok) break;
+            const int pos0 = cur.tile * C::KT;
+            const int first = pos0 >> a.kv.page_shift;
+            const int last = min(pos0 + C::KT, cur.len) - 1;
+            if (cur.n != ent_n || first < ent_base || (last >> a.kv.page_shift) >= ent_base + 32) {
+                ent_n = cur.n;
+                ent_base = first;
+                ent = 0;
+                if (ent_base + lane <= ((cur.len - 1) >> a.kv.page_shift))
+                    ent = a.kv.table[(int64_t)cur.n * a.kv.max_pages + ent_base + lane];
+            }
+            const int kvh = cur.sub / hb;
+            const int groups = min(boxes, (last - pos0) / rows_box + 1);
+            const int pos = pos0 + lg * rows_box;
+            const int page = __shfl_sync(0xffffffffu, ent, min(max((pos >> a.kv.page_shift) - ent_base, 0), 31));
+            uint8_t* tile = ring + st * C::kStage;
+            if (lane == 0) tc::mbar_expect_tx(&full[st], (uint32_t)(groups * rows_box * 128 * 2 * C::NB));
+            __syncwarp();
+            if (lg < groups) {
+                int64_t row = none;
+                if (page >= 0 && page < a.kv.n_pages)
+                    row = ((int64_t)page << a.kv.page_shift) + (pos & ((1 << a.kv.page_shift) - 1));
+                else
+                    atomicMax(&g_decode_attn_error, GDN_DEVERR_PAGE);
+                tc::tma_load_3d(tile + (lk * C::NB + lb) * C::kBlk + lg * rows_box * 128, lk ? &tv : &tk, &full[st],
+                                lb * (128 / (int)sizeof(IO)), kvh, (int)row);
+            }
+            cursor_next(a, cur, C::KT, subs, count - 1 - it);
+        }
+        if (!ok) {      // an expired wait: let every copy that was issued land before leaving
+            if (lane == 0) atomicMax(&g_decode_attn_error, GDN_DEVERR_TIMEOUT);
+            for (int i = 0; i < S; ++i) tc::mbar_wait(&full[i], 0, 1000000);
+        }
+        return;
+    }
+
+    // ---- consumers
+    const int team = warp >> 2, w = warp & 3;
+    Warp<IO, D, R> st;
+    const float sc = a.scale * kLog2e;
+    const Partials part = partials(a.ws, R, D);
+    bool ok = true, fresh = true, from_start = false;
+    for (int64_t it = 0; it < count; ++it) {
+        const int kvh = cur.sub / hb, h0 = kvh * G + (cur.sub - kvh * hb) * R;
+        const int rows = min(R, (kvh + 1) * G - h0);
+        const int64_t qrow = ((int64_t)cur.n * a.HQ + h0) * D;
+        if (fresh) {
+            from_start = cur.tile == 0;
+            if constexpr (sizeof(IO) == 4) {
+                // the rows' queries for every warp (rows past the group: zeros)
+                for (int i = tid; i < R * D; i += kConsumers) sq[i] = i < rows * D ? ((const float*)a.q)[qrow + i] : 0.f;
+                tc::named_bar(1, kConsumers);
+            }
+            st.start((const IO*)a.q + qrow, rows, sq);
+            fresh = false;
+        }
+        if ((int)(it & 1) == team) {
+            const int s = (int)(it % S);
+            if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], (uint32_t)((it / S) & 1)));
+            const int valid = min(C::KW, cur.len - cur.tile * C::KT - w * C::KW);
+            if (ok && valid > 0) st.step(ring + s * C::kStage, w, valid, rows, sc, sq);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&empty[s]);
+        }
+        const bool item_end = cur.tile + 1 == cur.tiles;
+        if (item_end || it + 1 == count) {
+            // the segment is over: join the eight warps
+            if (!ok && lane == 0) s_dead = 1;
+            st.put(merge + warp * R * (D + 4), rows);
+            tc::named_bar(1, kConsumers);
+            const bool whole = from_start && item_end;
+            const int64_t slot = (int64_t)blockIdx.x * 2 + (from_start ? 1 : 0);
+            for (int i = tid; i < rows * (D / 4); i += kConsumers) {
+                const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+                const float* p = merge + r * (D + 4);
+                float m = -INFINITY, l = 0.f;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < 8; ++k) m = fmaxf(m, p[k * R * (D + 4) + D]);
+                for (int k = 0; k < 8; ++k) {
+                    const float* pk = p + k * R * (D + 4);
+                    // a warp that took no key: m = -inf, l = 0, o = 0
+                    const float f = pk[D] == -INFINITY && pk[D + 1] == 0.f ? 0.f : exp2f(pk[D] - (m == -INFINITY ? 0.f : m));
+                    const float4 y = *reinterpret_cast<const float4*>(pk + c);
+                    if (f != 0.f || pk[D + 1] != 0.f) {
+                        l = fmaf(f, pk[D + 1], l);
+                        x.x = fmaf(f, y.x, x.x);
+                        x.y = fmaf(f, y.y, x.y);
+                        x.z = fmaf(f, y.z, x.z);
+                        x.w = fmaf(f, y.w, x.w);
+                    }
+                }
+                if (whole) {
+                    const float inv = 1.0f / l;
+                    const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int64_t at = qrow + (int64_t)r * D + c + e;
+                        store_elem((IO*)a.o, at, a.z ? gate_out(y[e], load_elem((const IO*)a.z, at)) : y[e]);
+                    }
+                } else {
+                    *reinterpret_cast<float4*>(part.o + (slot * R + r) * D + c) = x;
+                    if (c == 0) part.ml[slot * R + r] = make_float2(m, l);
+                }
+            }
+            tc::named_bar(1, kConsumers);
+            fresh = true;
+        }
+        cursor_next(a, cur, C::KT, subs, count - 1 - it);
+    }
+    if (s_dead && tid == 0) atomicMax(&g_decode_attn_error, GDN_DEVERR_TIMEOUT);
+}
+
+// Joins the pieces of the items that more than one block took.  Block (c, r): if block c of the
+// first kernel began inside an item, and is the first that did, row r of that item.
+constexpr int kJoinThreads = 256;
+template <typename IO, int D, int R>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int hb, int grid) {
+    constexpr int KT = Cfg<IO, D, R>::KT, E = D / 32;
+    __shared__ int64_t s_warp[kJoinThreads / 32];
+    __shared__ Place s_place;
+    __shared__ float s_o[8][D];
+    __shared__ float s_m[8], s_l[8];
+    tc::grid_dependency_sync();
+    const int c = blockIdx.x + 1, r = blockIdx.y, tid = threadIdx.x;
+    const int G = a.HQ / a.HKV, subs = a.HKV * hb;
+    int bad = 0;
+    int64_t begin;
+    const Place pl = find_place(
+        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, KT, &bad) * subs; }, c, grid, &begin, s_warp, &s_place);
+    if (pl.n < 0) return;
+    const int tiles = tiles_of(a, pl.n, KT, &bad);
+    const int64_t in_seq = begin - pl.before;
+    const int sub = (int)(in_seq / tiles);
+    const int64_t t0 = pl.before + (int64_t)sub * tiles, t1 = t0 + tiles;
+    // blocks that hold tiles of [t0, t1): the first is the last one that begins at or before t0
+    const int64_t N = pl.total;
+    const int c0 = (int)(((t0 + 1) * grid - 1) / N), c1 = (int)((t1 * grid - 1) / N);
+    auto start = [&](int b) { return N * b / grid; };
+    if (begin == t0 || c0 == c1) return;
+    int first = c0 + 1;                       // the first block that begins inside the item
+    while (start(first) == start(first + 1)) ++first;      // (blocks of no tiles hold nothing)
+    if (c != first) return;
+    const int kvh = sub / hb, h0 = kvh * G + (sub - kvh * hb) * R;
+    if (h0 + r >= (kvh + 1) * G) return;
+    const Partials part = partials(a.ws, R, D);
+    const int w = tid >> 5, lane = tid & 31;
+    auto slot = [&](int b) { return ((int64_t)b * 2 + (b == c0 ? 1 : 0)) * R + r; };
+    float m = -INFINITY;
+    for (int b = c0 + w * 32 + lane; b <= c1; b += kJoinThreads)
+        if (start(b) != start(b + 1)) m = fmaxf(m, part.ml[slot(b)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) s_m[w] = m;
+    __syncthreads();
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, s_m[i]);
+    const float base = m == -INFINITY ? 0.f : m;
+    float l = 0.f, x[E] = {};
+#pragma unroll 4
+    for (int b = c0 + w; b <= c1; b += 8) {
+        if (start(b) == start(b + 1)) continue;
+        const float2 ml = part.ml[slot(b)];
+        const float f = exp2f(ml.x - base);
+        const float* p = part.o + slot(b) * D + lane * E;
+        l = fmaf(f, ml.y, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fmaf(f, p[e], x[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = x[e];
+    if (lane == 0) s_l[w] = l;
+    __syncthreads();
+    if (tid < D) {
+        float y = 0.f, sum = 0.f;
+        for (int i = 0; i < 8; ++i) {
+            y += s_o[i][tid];
+            sum += s_l[i];
+        }
+        y /= sum;
+        const int64_t at = ((int64_t)pl.n * a.HQ + h0 + r) * D + tid;
+        store_elem((IO*)a.o, at, a.z ? gate_out(y, load_elem((const IO*)a.z, at)) : y);
+    }
+}
+
+template <typename IO, int D, int R>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+    using C = Cfg<IO, D, R>;
+    static_assert(C::kStages >= 4 && C::kSmem <= 226 * 1024, "decode: shared memory");
+    const int G = a.HQ / a.HKV, hb = (G + R - 1) / R;
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    // one block per SM, fewer where the longest contexts the tables can hold have fewer tiles
+    const int64_t most = (int64_t)a.n_seqs * a.HKV * hb * ((((int64_t)a.kv.max_pages << a.kv.page_shift) + C::KT - 1) / C::KT);
+    int grid = sms < kMaxGrid ? sms : kMaxGrid;
+    if (most < grid) grid = most > 0 ? (int)most : 1;
+    CUtensorMap tk, tv;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.HKV, (cuuint64_t)a.kv.n_pages << a.kv.page_shift};
+    const cuuint64_t str[2] = {(cuuint64_t)D * sizeof(IO), (cuuint64_t)a.HKV * D * sizeof(IO)};
+    const int page = 1 << a.kv.page_shift;
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(IO)), 1, (cuuint32_t)(page < C::KT ? page : C::KT)};
+    const CUtensorMapDataType dt = sizeof(IO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    if (!make_map(&tk, dt, a.kv.k, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_map(&tv, dt, a.kv.v, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    e = cudaFuncSetAttribute(attn_decode_kernel<IO, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<IO, D, R>, tk, tv, a, hb);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    if (grid == 1) return cudaSuccess;           // nothing to join
+    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(G < R ? G : R));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<IO, D, R>, a, hb, grid);
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+template <int D>
+cudaError_t launch_f32(const AttnArgs& a, cudaStream_t s) {
+    // rows cost registers and work in the fp32 kernel, used or not: the smallest count that holds
+    // the group, at most 8
+    const int G = a.HQ / a.HKV;
+    if (G == 1) return launch<float, D, 1>(a, s);
+    if (G <= 4) return launch<float, D, 4>(a, s);
+    return launch<float, D, 8>(a, s);
+}
+
+}  // namespace
+
+size_t attn_decode_bytes(int D) {
+    return kStatusBytes + (size_t)kMaxGrid * 2 * 16 * (sizeof(float2) + (size_t)D * 4);
+}
+
+cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
+    if (a.bf16) return a.D == 128 ? launch<bf16, 128, 16>(a, s) : launch<bf16, 64, 16>(a, s);
+    return a.D == 128 ? launch_f32<128>(a, s) : launch_f32<64>(a, s);
+}
+
+cudaError_t read_attn_decode_error(int32_t* out) {
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_decode_attn_error, sizeof(int32_t));
+    if (e == cudaSuccess && *out != 0) {
+        const int32_t zero = 0;
+        e = cudaMemcpyToSymbol(g_decode_attn_error, &zero, sizeof(int32_t));
+    }
+    return e;
+}
+
+}  // namespace gdn

@@ -448,7 +448,12 @@ def test_bad_tables_are_reported_and_stay_contained(dtype):
         o = torch.full_like(q, 7.0)
         G.gdn_attn_decode(q, c.k, c.v, c.table, lens, o=o)
         assert G.gdn_attn_status() == 3
-        assert torch.equal(o[[0, 2]], good[[0, 2]]) and (o[1] == 7.0).all()
+        # (the lengths of a batch decide where its work is split, so the others' sums may be taken
+        # in another order: the reference's bound, not the same bits)
+        for i in (0, 2):
+            kn, vn = c.seq(i)
+            _check_rows(o[i:i + 1], q[i:i + 1], kn, vn, c.totals[i] - 1, 128 ** -0.5, dtype, None, f"sequence {i}")
+        assert (o[1] == 7.0).all()
         k, v = _draw(g, (3, 2, 128), dtype), _draw(g, (3, 2, 128), dtype)
         kc, vc = c.k.clone(), c.v.clone()
         qo = torch.full_like(q, 7.0)
