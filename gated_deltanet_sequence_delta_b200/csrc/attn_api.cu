@@ -78,7 +78,20 @@ gdn_status check_attn(const AttnArgs& a, gdn_dtype io, size_t need, void* worksp
 
 size_t prefill_bytes(int64_t n_tokens, int32_t n_seqs, int32_t HQ, int32_t HKV, int32_t D, gdn_dtype io) {
     if (n_tokens < 0 || n_tokens > INT32_MAX || n_seqs < 0 || check_heads(io, HQ, HKV, D) != GDN_OK) return 0;
+    // the kernels count tiles (of one token or more, per key-value head) in 32 bits
+    if ((n_tokens + n_seqs) * (int64_t)HQ > INT32_MAX) return 0;
+    if (io == GDN_BF16 && gdn::attn_tc_supported(HQ, HKV)) return gdn::attn_tc_bytes(n_tokens, n_seqs, HQ, HKV);
     return gdn::attn_cudacore_bytes(n_tokens, n_seqs, HQ, HKV);
+}
+
+// A prompt call whose sizes are checked.
+gdn_status run_prefill(const AttnArgs& a, gdn_dtype io, void* workspace, size_t workspace_bytes, void* stream) {
+    const size_t need = prefill_bytes(a.n_tokens, a.n_seqs, a.HQ, a.HKV, a.D, io);
+    if (need == 0) return GDN_ERR_UNSUPPORTED;
+    const gdn_status st = check_attn(a, io, need, workspace, workspace_bytes);
+    if (st != GDN_OK) return st;
+    if (a.bf16 && gdn::attn_tc_supported(a.HQ, a.HKV)) return cuda_status(gdn::launch_attn_tc(a, (cudaStream_t)stream));
+    return cuda_status(gdn::launch_attn_cudacore(a, (cudaStream_t)stream));
 }
 
 size_t decode_bytes(int32_t B, int32_t HQ, int32_t HKV, int32_t D, gdn_dtype io) {
@@ -149,9 +162,7 @@ gdn_status gdn_attn_prefill(const void* q, const void* k, const void* v, gdn_dty
     if (n_tokens == 0 || n_seqs == 0) return GDN_OK;
     const AttnArgs a{q, {k, v, nullptr, nullptr, 0, 0, 0}, cu_seqlens, T, n_tokens, n_seqs, HQ, HKV, D, scale, z, o,
                      io_dtype == GDN_BF16, workspace};
-    st = check_attn(a, io_dtype, prefill_bytes(n_tokens, n_seqs, HQ, HKV, D, io_dtype), workspace, workspace_bytes);
-    if (st != GDN_OK) return st;
-    return cuda_status(gdn::launch_attn_cudacore(a, (cudaStream_t)stream));
+    return run_prefill(a, io_dtype, workspace, workspace_bytes, stream);
 }
 
 gdn_status gdn_attn_prefill_paged(const void* q, gdn_dtype io_dtype, const void* k_cache, const void* v_cache,
@@ -169,9 +180,7 @@ gdn_status gdn_attn_prefill_paged(const void* q, gdn_dtype io_dtype, const void*
     if (!block_table || !kv_lens || !cu_seqlens) return GDN_ERR_NULL;
     const AttnArgs a{q, {k_cache, v_cache, block_table, kv_lens, n_pages, page_shift_of(page_size), max_pages},
                      cu_seqlens, 0, n_tokens, n_seqs, HQ, HKV, D, scale, z, o, io_dtype == GDN_BF16, workspace};
-    st = check_attn(a, io_dtype, prefill_bytes(n_tokens, n_seqs, HQ, HKV, D, io_dtype), workspace, workspace_bytes);
-    if (st != GDN_OK) return st;
-    return cuda_status(gdn::launch_attn_cudacore(a, (cudaStream_t)stream));
+    return run_prefill(a, io_dtype, workspace, workspace_bytes, stream);
 }
 
 size_t gdn_attn_decode_workspace_bytes(int32_t B, int32_t HQ, int32_t HKV, int32_t D, gdn_dtype io_dtype) {
@@ -202,7 +211,8 @@ gdn_status gdn_attn_status(int32_t* device_error) {
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_status(e);
     int32_t word = 0;
-    for (auto read : {gdn::read_append_error, gdn::read_attn_cudacore_error, gdn::read_attn_decode_error}) {
+    for (auto read : {gdn::read_append_error, gdn::read_attn_cudacore_error, gdn::read_attn_decode_error,
+                      gdn::read_attn_tc_error}) {
         int32_t w = 0;
         e = read(&w);
         if (e != cudaSuccess) return cuda_status(e);

@@ -61,7 +61,7 @@ struct AttnPlan {
     int32_t* counts;
     int2* tiles;
     int4* redo;
-    int max_tiles;
+    int max_tiles, max_redo;
     size_t bytes;
 };
 // Tiles of `tile_rows` rows, `row_per_tok` rows a token.
@@ -73,6 +73,12 @@ __device__ __forceinline__ float gate_out(float o, float z) { return o / (1.0f +
 
 cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
+// bf16 on the tensor cores; the query heads of a group have to fit a tile's rows.
+bool attn_tc_supported(int HQ, int HKV);
+size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
+cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
+// Redo the tiles (of tile_tokens tokens by the group's heads) that the plan lists, on CUDA cores.
+cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, int tile_tokens, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_decode_bytes(int D);
 size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
@@ -81,5 +87,6 @@ size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
 cudaError_t read_append_error(int32_t* out);
 cudaError_t read_attn_cudacore_error(int32_t* out);
 cudaError_t read_attn_decode_error(int32_t* out);
+cudaError_t read_attn_tc_error(int32_t* out);
 
 }  // namespace gdn

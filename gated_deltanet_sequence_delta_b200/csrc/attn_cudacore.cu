@@ -233,6 +233,22 @@ __global__ void __launch_bounds__(kThreads) attn_cc_kernel(AttnArgs a, AttnPlan 
     attn_tile<IO, D>(a, sm, sq, it.x, blockIdx.y, (int64_t)it.y * kM, G, blockIdx.y * G, (int64_t)sq.n_q * G);
 }
 
+// The tiles that the tensor-core kernel listed, 64 rows a block at a time.
+template <int D>
+__global__ void __launch_bounds__(kThreads) attn_redo_kernel(AttnArgs a, AttnPlan plan, int tile_tokens) {
+    extern __shared__ float4 smem_raw[];
+    Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+    const int G = a.HQ / a.HKV, parts = (tile_tokens * G + kM - 1) / kM;
+    const int64_t count = (int64_t)min(plan.counts[1], plan.max_redo) * parts;
+    for (int64_t i = blockIdx.x; i < count; i += gridDim.x) {
+        const int4 it = plan.redo[i / parts];
+        const SeqRows sq = seq_rows(a, it.x);
+        const int64_t first = (int64_t)it.y * tile_tokens * G, end = min(first + tile_tokens * G, (int64_t)sq.n_q * G);
+        const int64_t row0 = first + (i % parts) * kM;
+        if (row0 < end) attn_tile<__nv_bfloat16, D>(a, sm, sq, it.x, it.z, row0, G, it.z * G, end);
+    }
+}
+
 // The plan: every sequence's tiles, the longest key ranges first (the grid starts them in
 // order, so the short ones fill the end).  Counting sort over kBuckets lengths; the order
 // inside a bucket varies and changes no result.
@@ -302,6 +318,7 @@ AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int heads, int row_pe
     const int64_t tiles = (n_tokens * row_per_tok + tile_rows - 1) / tile_rows + n_seqs;
     uint8_t* b = static_cast<uint8_t*>(ws);
     p.max_tiles = (int)tiles;
+    p.max_redo = (int)(tiles * heads);
     p.counts = reinterpret_cast<int32_t*>(b);
     size_t at = kStatusBytes;
     p.tiles = reinterpret_cast<int2*>(b + at);
@@ -315,6 +332,22 @@ AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int heads, int row_pe
 cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s) {
     attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, p, row_per_tok, tile_rows);
     const cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) count_launch();
+    return e;
+}
+
+cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, int tile_tokens, cudaStream_t s) {
+    const void* f = a.D == 128 ? (const void*)attn_redo_kernel<128> : (const void*)attn_redo_kernel<64>;
+    const size_t smem = a.D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    // the list is empty unless something is not finite: a grid that starts and ends in about the
+    // launch's own time (2 us), and still spreads a list over the device
+    if (a.D == 128)
+        attn_redo_kernel<128><<<148, kThreads, smem, s>>>(a, p, tile_tokens);
+    else
+        attn_redo_kernel<64><<<148, kThreads, smem, s>>>(a, p, tile_tokens);
+    e = cudaGetLastError();
     if (e == cudaSuccess) count_launch();
     return e;
 }

@@ -7,7 +7,8 @@ kernels' result o differs from the exact one by at most
     A * (r_P + 2 e_s + (n + 16) u) + |o| (r_out + 16 u),      u = 2^-24
 
 * r_P: the weights are rounded to bf16 before the product with v in the bf16 mode (half a
-  step, 2^-8 relative), not at all in fp32;
+  step, 2^-8 relative), and a share of them is formed by a cubic that is off by at most
+  7.5e-5 relative, in the numerator and in the sum (twice); neither in fp32;
 * e_s: a score is a sum of D products in fp32, each term and each partial sum rounded:
   |ds| <= (D + 3) u scale sum_d |q_d k_d|, which moves a weight by the factor e^ds, and the
   row's sum by no more: 2 e_s in all (the scores' products are exact: bf16 times bf16, or
@@ -40,7 +41,7 @@ def attention(q, k, v, past, scale, dtype, z=None):
     n, HQ, D = q.shape
     G = HQ // k.shape[1]
     o, bound = np.zeros(q.shape), np.zeros(q.shape)
-    r_p = HALF_STEP["bf16"] if dtype == "bf16" else 0.0
+    r_p = HALF_STEP["bf16"] + 2 * 7.5e-5 if dtype == "bf16" else 0.0
     for i in range(n):
         m = max(past + i + 1, 0)
         for h in range(HQ):
