@@ -55,8 +55,9 @@ __device__ __forceinline__ SeqRows seq_rows(const AttnArgs& a, int n) {
 }
 
 // Scratch of the prompt attentions, built by the plan kernel and filled in by the main one:
-// word 0 the number of tiles, word 1 the number of tiles to redo, then {sequence, tile} pairs
-// (longest key range first), then {sequence, head, first token, 0} records of tiles to redo.
+// word 0 the number of tiles, word 1 the number of records to redo, then {sequence, tile} pairs
+// (longest key range first), then {sequence, key-value head, first row, rows} records to redo
+// (rows of that head's (token, query head) rows of the sequence).
 struct AttnPlan {
     int32_t* counts;
     int2* tiles;
@@ -64,9 +65,26 @@ struct AttnPlan {
     int max_tiles, max_redo;
     size_t bytes;
 };
-// Tiles of `tile_rows` rows, `row_per_tok` rows a token.
-AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int heads, int row_per_tok, int tile_rows);
+// Tiles of `tile_rows` rows, `row_per_tok` rows a token; room for `redo` records a tile.
+AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows);
 cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s);
+
+// Launch with programmatic stream serialisation: the kernel may start while the one before it
+// drains, and waits in griddepcontrol.wait before it touches memory.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*f)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, f, args...);
+}
 
 // out * sigmoid(z)
 __device__ __forceinline__ float gate_out(float o, float z) { return o / (1.0f + expf(-z)); }
@@ -77,8 +95,8 @@ cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
 bool attn_tc_supported(int HQ, int HKV);
 size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
-// Redo the tiles (of tile_tokens tokens by the group's heads) that the plan lists, on CUDA cores.
-cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, int tile_tokens, cudaStream_t s);
+// Redo the rows that the plan lists, on CUDA cores.
+cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_decode_bytes(int D);
 size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);

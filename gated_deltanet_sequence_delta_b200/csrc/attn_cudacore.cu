@@ -13,6 +13,7 @@
 // Masked places never enter a sum, neither their scores nor 0 * v_j, so infinities and NaN in
 // values a row does not see leave it alone.
 #include "attn_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -226,6 +227,7 @@ template <typename IO, int D>
 __global__ void __launch_bounds__(kThreads) attn_cc_kernel(AttnArgs a, AttnPlan plan) {
     extern __shared__ float4 smem_raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
+    tc::grid_dependency_sync();
     if ((int)blockIdx.x >= plan.counts[0]) return;
     const int2 it = plan.tiles[blockIdx.x];
     const SeqRows sq = seq_rows(a, it.x);
@@ -233,19 +235,18 @@ __global__ void __launch_bounds__(kThreads) attn_cc_kernel(AttnArgs a, AttnPlan 
     attn_tile<IO, D>(a, sm, sq, it.x, blockIdx.y, (int64_t)it.y * kM, G, blockIdx.y * G, (int64_t)sq.n_q * G);
 }
 
-// The tiles that the tensor-core kernel listed, 64 rows a block at a time.
+// The rows that the tensor-core kernel listed.
 template <int D>
-__global__ void __launch_bounds__(kThreads) attn_redo_kernel(AttnArgs a, AttnPlan plan, int tile_tokens) {
+__global__ void __launch_bounds__(kThreads) attn_redo_kernel(AttnArgs a, AttnPlan plan) {
     extern __shared__ float4 smem_raw[];
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
-    const int G = a.HQ / a.HKV, parts = (tile_tokens * G + kM - 1) / kM;
-    const int64_t count = (int64_t)min(plan.counts[1], plan.max_redo) * parts;
-    for (int64_t i = blockIdx.x; i < count; i += gridDim.x) {
-        const int4 it = plan.redo[i / parts];
+    tc::grid_dependency_sync();
+    const int G = a.HQ / a.HKV, count = min(plan.counts[1], plan.max_redo);
+    for (int i = blockIdx.x; i < count; i += gridDim.x) {
+        const int4 it = plan.redo[i];
         const SeqRows sq = seq_rows(a, it.x);
-        const int64_t first = (int64_t)it.y * tile_tokens * G, end = min(first + tile_tokens * G, (int64_t)sq.n_q * G);
-        const int64_t row0 = first + (i % parts) * kM;
-        if (row0 < end) attn_tile<__nv_bfloat16, D>(a, sm, sq, it.x, it.z, row0, G, it.z * G, end);
+        const int64_t end = min((int64_t)it.z + it.w, (int64_t)sq.n_q * G);
+        if (it.z < end) attn_tile<__nv_bfloat16, D>(a, sm, sq, it.x, it.y, it.z, G, it.y * G, end);
     }
 }
 
@@ -260,6 +261,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Att
     for (int i = tid; i < kBuckets; i += kPlanThreads) s_count[i] = 0;
     if (tid == 0) s_max = 1;
     __syncthreads();
+    tc::grid_dependency_sync();
     int mx = 1;
     for (int n = tid; n < a.n_seqs; n += kPlanThreads) {
         const SeqRows r = seq_rows(a, n);
@@ -305,49 +307,44 @@ cudaError_t launch_cc(const AttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<IO, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)sizeof(Smem<D>));
     if (e != cudaSuccess) return e;
-    attn_cc_kernel<IO, D><<<dim3((unsigned)plan.max_tiles, (unsigned)a.HKV), kThreads, sizeof(Smem<D>), s>>>(a, plan);
-    e = cudaGetLastError();
+    e = launch_pdl(attn_cc_kernel<IO, D>, dim3((unsigned)plan.max_tiles, (unsigned)a.HKV), dim3(kThreads),
+                   sizeof(Smem<D>), s, a, plan);
     if (e == cudaSuccess) count_launch();
     return e;
 }
 
 }  // namespace
 
-AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int heads, int row_per_tok, int tile_rows) {
+AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows) {
     AttnPlan p;
     const int64_t tiles = (n_tokens * row_per_tok + tile_rows - 1) / tile_rows + n_seqs;
     uint8_t* b = static_cast<uint8_t*>(ws);
     p.max_tiles = (int)tiles;
-    p.max_redo = (int)(tiles * heads);
+    p.max_redo = (int)(tiles * redo);
     p.counts = reinterpret_cast<int32_t*>(b);
     size_t at = kStatusBytes;
     p.tiles = reinterpret_cast<int2*>(b + at);
     at += (size_t)((tiles * sizeof(int2) + 255) / 256 * 256);
     p.redo = reinterpret_cast<int4*>(b + at);
-    at += (size_t)(((size_t)tiles * heads * sizeof(int4) + 255) / 256 * 256);
+    at += (size_t)(((size_t)tiles * redo * sizeof(int4) + 255) / 256 * 256);
     p.bytes = at;
     return p;
 }
 
 cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s) {
-    attn_plan_kernel<<<1, kPlanThreads, 0, s>>>(a, p, row_per_tok, tile_rows);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, row_per_tok, tile_rows);
     if (e == cudaSuccess) count_launch();
     return e;
 }
 
-cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, int tile_tokens, cudaStream_t s) {
-    const void* f = a.D == 128 ? (const void*)attn_redo_kernel<128> : (const void*)attn_redo_kernel<64>;
+cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     const size_t smem = a.D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>);
+    const auto f = a.D == 128 ? attn_redo_kernel<128> : attn_redo_kernel<64>;
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     // the list is empty unless something is not finite: a grid that starts and ends in about the
-    // launch's own time (2 us), and still spreads a list over the device
-    if (a.D == 128)
-        attn_redo_kernel<128><<<148, kThreads, smem, s>>>(a, p, tile_tokens);
-    else
-        attn_redo_kernel<64><<<148, kThreads, smem, s>>>(a, p, tile_tokens);
-    e = cudaGetLastError();
+    // launch's own time, and still spreads a list over the device
+    e = launch_pdl(f, dim3(148), dim3(kThreads), smem, s, a, p);
     if (e == cudaSuccess) count_launch();
     return e;
 }

@@ -661,24 +661,12 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     e = cudaFuncSetAttribute(attn_decode_kernel<IO, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = C::kSmem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attn_decode_kernel<IO, D, R>, tk, tv, a, hb);
+    e = launch_pdl(attn_decode_kernel<IO, D, R>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tk, tv, a, hb);
     if (e != cudaSuccess) return e;
     count_launch();
     if (grid == 1) return cudaSuccess;           // nothing to join
-    cfg.gridDim = dim3((unsigned)(grid - 1), (unsigned)(G < R ? G : R));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<IO, D, R>, a, hb, grid);
+    e = launch_pdl(attn_join_kernel<IO, D, R>, dim3((unsigned)(grid - 1), (unsigned)(G < R ? G : R)), dim3(kJoinThreads), 0,
+                   s, a, hb, grid);
     if (e == cudaSuccess) count_launch();
     return e;
 }

@@ -12,15 +12,20 @@
 // 128 / G tokens by G heads, so that the group shares every key and value that is staged and
 // the diagonal's waste shrinks with G (rows left over where G does not divide 128 are idle).  A
 // block takes two consecutive tiles, A and B, against the same keys: while the softmax of one
-// runs, the tensor cores work for the other.
+// runs, the tensor cores work for the other.  Blocks are persistent, so that an item's first
+// loads and scores run under the last item's outputs.
 //
-// Roles (12 warps, one block per SM; warps 10 and 11 only complete a warpgroup):
-//   warps 0-3, 4-7   softmax of tile A, of tile B: a thread owns a row (TMEM lane), reads its 128
-//                    scores, forms the weights, writes them as bf16 over the scores
-//   warp 8           issues the MMAs: per step  O_A += P_A V,  S_A = Q_A K',  O_B += P_B V,
-//                    S_B = Q_B K'  (K' the next keys)
-//   warp 9           TMA: queries once, then keys and values through a ring
-// TMEM: S_A, S_B (128 columns each, the weights in the first 64), O_A, O_B (D columns each).
+// Roles (12 warps, one block per SM; the last only completes a warpgroup):
+//   warps 0-3, 4-7   softmax of tile A, of tile B: a thread owns a row (TMEM lane), takes its 128
+//                    scores into registers, forms the weights, writes them as bf16
+//   warps 8, 9       issue the MMAs of tile A, of tile B: per step  S = Q K',  O += P V  (K' the
+//                    next step's keys); two warps, so that neither tile's products wait behind
+//                    the other's softmax
+//   warp 10          TMA: queries once, then keys and values through a ring
+// TMEM, 512 columns: S 128, P_A and P_B 64 each, O_A and O_B D each.  A tile's scores of the next
+// step are formed while its softmax works on the last ones, so that the products stay off that
+// chain; at D = 128 this leaves room for one S, which the tiles use in turn (it is free again
+// once its softmax warps have read it), at D = 64 for one each.
 //
 // The reference m moves only when a row's maximum has grown by more than 2^8 since it was set:
 // weights then stay below 2^8, sums and products in fp32 lose nothing, and the accumulated O has
@@ -56,6 +61,11 @@ struct Cfg {
     static constexpr int kHalf = 128 * 128;                      // bytes of one column block
     static constexpr int kRing = D == 128 ? 5 : 8;               // key / value tiles
     static constexpr int kSmem = (2 + kRing) * kTile + 1024;
+    static constexpr bool kOneS = D == 128;                      // one S for both tiles
+    // TMEM columns
+    __device__ static constexpr int s_col(int x) { return kOneS ? 0 : x * 128; }
+    __device__ static constexpr int p_col(int x) { return (kOneS ? 128 : 256) + x * 64; }
+    __device__ static constexpr int o_col(int x) { return 512 - 2 * D + x * D; }
 };
 
 // 2^x for two floats, |x| < 126 or x < 0 (below 2^-126 it stays there): x = n + f, n the nearest
@@ -111,30 +121,67 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return r;
 }
 
-// The block's work: tiles A and B of one (sequence, tile pair, key-value head).
-struct Item {
-    SeqRows sq;
-    int n, kvh, past;
-    int tok[2], ntok[2];       // first token of each tile, tokens in it (0: no tile)
-    int steps[2];              // key steps of each tile
-    int total;
-};
-__device__ __forceinline__ Item item_of(const AttnArgs& a, int n, int pair, int kvh, int tokens) {
-    Item it;
-    it.n = n;
-    it.kvh = kvh;
-    it.sq = seq_rows(a, n);
-    it.past = it.sq.n_kv - it.sq.n_q;
-    it.total = 0;
+// A row's weights 2^(s sc - base) as bf16 in tensor memory (keys 2j, 2j + 1 in column j); returns
+// their sum.  `free` is called before the first write.  MASKED: keys past `last` weigh exactly 0,
+// and all the others go through the special-function units (the cubic does not reach 0).
+template <bool MASKED, typename F>
+__device__ __forceinline__ float weights(const float (&s)[128], float sc, float base, int last, uint32_t tp, F free) {
+    const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
+    uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        it.tok[x] = (pair * 2 + x) * tokens;
-        it.ntok[x] = max(min(tokens, it.sq.n_q - it.tok[x]), 0);
-        const int end = it.ntok[x] > 0 ? max(it.past + it.tok[x] + it.ntok[x], 0) : 0;    // keys its last row sees
-        it.steps[x] = (end + kKeys - 1) / kKeys;
-        it.total = max(it.total, it.steps[x]);
+    for (int c = 0; c < 128; c += 32) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+            float e0, e1;
+            unpack2(fma2(pack2(s[c + j], s[c + j + 1]), sc2, nb2), e0, e1);
+            if (MASKED) {
+                e0 = c + j > last ? 0.f : exp2_sfu(e0);
+                e1 = c + j + 1 > last ? 0.f : exp2_sfu(e1);
+            } else if ((j & 7) == 6) {
+                exp2_poly(e0, e1);
+            } else {
+                e0 = exp2_sfu(e0);
+                e1 = exp2_sfu(e1);
+            }
+            sum[(j >> 1) & 3] = add2(sum[(j >> 1) & 3], pack2(e0, e1));
+            p[j / 2] = pack_bf16(e0, e1);
+        }
+        if (c == 0) free();
+        tc::tmem_st16_raw(tp + c / 2, p);
     }
-    return it;
+    float a, b;
+    unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, b);
+    return a + b;
+}
+
+// One item of a block's work: tiles A and B of a (sequence, tile pair, key-value head).
+struct Item {
+    int n, kvh, q0, n_q, n_kv, past;
+    int tok;                   // first token of A; B follows `tokens` later
+    int tokens;
+    // of tile x: tokens it has (0: no tile), keys its last row sees, steps of 128 keys
+    __device__ __forceinline__ int ntok(int x) const { return max(min(tokens, n_q - tok - x * tokens), 0); }
+    __device__ __forceinline__ int end(int x) const { return ntok(x) > 0 ? max(past + tok + x * tokens + ntok(x), 0) : 0; }
+    __device__ __forceinline__ int steps(int x) const { return (end(x) + kKeys - 1) / kKeys; }
+    __device__ __forceinline__ int total() const { return max(steps(0), steps(1)); }
+};
+// The r-th item of this block.  The list runs from long to short; blocks take it forwards and
+// backwards in turn, which evens out their sums.
+__device__ __forceinline__ bool item_at(const AttnArgs& a, const AttnPlan& plan, int count, int tokens, int r, Item& it) {
+    const int64_t i = (int64_t)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (i >= count) return false;
+    const int2 pt = plan.tiles[i / a.HKV];
+    const SeqRows sq = seq_rows(a, pt.x);
+    it.n = pt.x;
+    it.kvh = (int)(i % a.HKV);
+    it.q0 = sq.q0;
+    it.n_q = sq.n_q;
+    it.n_kv = sq.n_kv;
+    it.past = sq.n_kv - sq.n_q;
+    it.tok = pt.y * 2 * tokens;
+    it.tokens = tokens;
+    return true;
 }
 
 template <int D>
@@ -143,33 +190,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                                                                    const __grid_constant__ CUtensorMap tv, AttnArgs a,
                                                                    AttnPlan plan, int tokens, int box_rows) {
     using C = Cfg<D>;
+    constexpr int S = C::kRing;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t q_full, kv_full[C::kRing], kv_empty[C::kRing], s_full[2], p_full[2], o_full[2],
-        drain;
+    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], s_read[2], p_full[2], pv_done[2],
+        drain[2];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_redo, s_timeout;
+    __shared__ int s_timeout;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    if ((int)(blockIdx.x / a.HKV) >= plan.counts[0]) return;
     uint8_t* q_smem = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     uint8_t* ring = q_smem + 2 * C::kTile;
     const int G = a.HQ / a.HKV;
-    const int2 pt = plan.tiles[blockIdx.x / a.HKV];
-    const Item it = item_of(a, pt.x, pt.y, blockIdx.x % a.HKV, tokens);
 
     if (tid == 0) {
         tc::mbar_init(&q_full, 1);
-        for (int i = 0; i < C::kRing; ++i) {
+        tc::mbar_init(&q_empty, 2);
+        for (int i = 0; i < S; ++i) {
             tc::mbar_init(&kv_full[i], 1);
-            tc::mbar_init(&kv_empty[i], 1);
+            tc::mbar_init(&kv_empty[i], 2);
         }
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(&s_full[x], 1);
+            tc::mbar_init(&s_read[x], 4);
             tc::mbar_init(&p_full[x], 4);
-            tc::mbar_init(&o_full[x], 1);
+            tc::mbar_init(&pv_done[x], 1);
         }
-        tc::mbar_init(&drain, 1);
+        tc::mbar_init(&drain[0], 1);
+        tc::mbar_init(&drain[1], 1);
         tc::fence_mbar_init();
-        s_redo = 0;
         s_timeout = 0;
     }
     if (warp == 8) {
@@ -180,228 +227,265 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
+    tc::grid_dependency_sync();          // the plan is ready, and what ran before has left o alone
+    const int count = plan.counts[0] * a.HKV;
 
     if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-    if (warp == 9) {
-        // ---- loads --------------------------------------------------------------------
-        bool ok = true;
-        if (lane == 0 && it.total > 0) {
-            tc::mbar_expect_tx(&q_full, (uint32_t)((it.ntok[1] > 0 ? 2 : 1) * C::kHalves * tokens * G * 128));
-            for (int x = 0; x < 2; ++x)
-                if (it.ntok[x] > 0)
-                    for (int h = 0; h < C::kHalves; ++h)
-                        tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tq, &q_full, h * 64, it.kvh * G,
-                                        it.sq.q0 + it.tok[x]);
-        }
-        const int boxes = kKeys / box_rows;
-        const int lg = lane / C::kHalves, lh = lane % C::kHalves;      // this lane's box, its column block
-        const int none = a.kv.table ? (int)((int64_t)a.kv.n_pages << a.kv.page_shift) : 0;
-        for (int t = 0; t < 2 * it.total; ++t) {                        // K_0, V_0, K_1, V_1, ...
-            const int s = t % C::kRing;
-            if (t >= C::kRing) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], (uint32_t)((t / C::kRing) & 1) ^ 1u));
-            if (!ok) break;
-            const int pos = (t >> 1) * kKeys + lg * box_rows;
-            uint8_t* dst = ring + s * C::kTile + lh * C::kHalf + lg * box_rows * 128;
-            int row = it.sq.q0 + pos;
-            if (a.kv.table && lg < boxes) {
-                row = none;                                             // past the cache: zero fill
-                if (pos < it.sq.n_kv) {
-                    const int64_t r = cache_row(a.kv.table + (int64_t)it.n * a.kv.max_pages, pos, a.kv.page_shift,
-                                                a.kv.n_pages);
-                    if (r >= 0)
-                        row = (int)r;
-                    else
-                        atomicMax(&g_attn_tc_error, GDN_DEVERR_PAGE);
-                }
-            }
-            if (lane == 0) tc::mbar_expect_tx(&kv_full[s], C::kTile);
-            __syncwarp();
-            if (lg < boxes) tc::tma_load_3d(dst, (t & 1) ? &tv : &tk, &kv_full[s], lh * 64, it.kvh, row);
-        }
-        if (!ok) {
-            if (lane == 0) s_timeout = 1;
-            for (int i = 0; i < C::kRing; ++i) tc::mbar_wait(&kv_full[i], 0, 1000000);
-        }
-    } else if (warp == 8) {
-        // ---- products -----------------------------------------------------------------
-        if (lane == 0 && it.total > 0) {
-            const uint32_t neg = a.scale < 0.f ? 1u << 13 : 0u;         // -Q: scores of a negative scale
-            const uint32_t id_s = tc::idesc_bf16(128, kKeys, 0, 0) | neg, id_o = tc::idesc_bf16(128, D, 0, 1);
-            bool ok = tc::mbar_wait(&q_full, 0);
-            auto scores = [&](int x, int t) {                           // S_x = Q_x K^T, keys in ring tile t
-                const uint32_t qa = tc::smem_u32(q_smem + x * C::kTile);
-                const uint32_t kb = tc::smem_u32(ring + (t % C::kRing) * C::kTile);
-#pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint32_t off = (k >> 2) * C::kHalf + (k & 3) * 32;
-                    tc::mma_bf16(tmem + x * 128, tc::desc_sw128(qa + off, 0, 1024), tc::desc_sw128(kb + off, 0, 1024),
-                                 id_s, k > 0);
-                }
-                tc::mma_commit(&s_full[x]);
-            };
-            auto outputs = [&](int x, int t, bool acc) {                // O_x += P_x V, values in ring tile t
-                const uint32_t vb = tc::smem_u32(ring + (t % C::kRing) * C::kTile);
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k)
-                    tc::mma_bf16_ts(tmem + 256 + x * D, tmem + x * 128 + k * 8,
-                                    tc::desc_sw128(vb + k * 2048, C::kHalf, 1024), id_o, acc || k > 0);
-            };
-            auto wait_kv = [&](int t) {
-                if (ok) ok = tc::mbar_wait(&kv_full[t % C::kRing], (uint32_t)((t / C::kRing) & 1));
-                tc::tc_fence_after();
-            };
-            wait_kv(0);
-            for (int x = 0; x < 2 && ok; ++x)
-                if (it.steps[x] > 0) scores(x, 0);
-            if (ok && C::kRing < 2 * it.total) tc::mma_commit(&kv_empty[0]);
-            for (int i = 0; i < it.total && ok; ++i) {
-                wait_kv(2 * i + 1);
-                bool have_k = false;
-                for (int x = 0; x < 2 && ok; ++x) {
-                    if (i >= it.steps[x]) continue;
-                    ok = tc::mbar_wait_spin(&p_full[x], (uint32_t)(i & 1));
-                    if (!ok) break;
-                    tc::tc_fence_after();
-                    outputs(x, 2 * i + 1, i > 0);
-                    if (i + 1 == it.steps[x]) tc::mma_commit(&o_full[x]);
-                    if (i + 1 < it.steps[x]) {
-                        if (!have_k) wait_kv(2 * i + 2);
-                        have_k = true;
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        if (warp == 10) {
+            // ---- loads ------------------------------------------------------------------
+            bool ok = true;
+            const int boxes = kKeys / box_rows;
+            const int lg = lane / C::kHalves, lh = lane % C::kHalves;  // this lane's box, its column block
+            const int none = (int)((int64_t)a.kv.n_pages << a.kv.page_shift);
+            int t = 0, items = 0;
+            Item it;
+            for (int r = 0; ok && item_at(a, plan, count, tokens, r, it); ++r) {
+                const int total = it.total();
+                for (int u = 0; u < 2 * total; ++u, ++t) {             // K_0, (Q), K_1, V_0, K_2, V_1, ..., V_last
+                    const bool is_v = u + 1 == 2 * total || (u > 0 && (u & 1) == 0);
+                    const int step = u + 1 == 2 * total ? total - 1 : is_v ? (u >> 1) - 1 : (u + 1) >> 1;
+                    if (u == 1) {
+                        if (items > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty, (uint32_t)(items - 1) & 1u));
                         if (!ok) break;
-                        scores(x, 2 * i + 2);
+                        if (lane == 0) {
+                            const int tiles = it.ntok(1) > 0 ? 2 : 1;
+                            tc::mbar_expect_tx(&q_full, (uint32_t)(tiles * C::kHalves * tokens * G * 128));
+                            for (int x = 0; x < tiles; ++x)
+                                for (int h = 0; h < C::kHalves; ++h)
+                                    tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tq, &q_full, h * 64, it.kvh * G,
+                                                    it.q0 + it.tok + x * tokens);
+                        }
+                        __syncwarp();
+                        ++items;
                     }
+                    const int s = t % S;
+                    const int pos = step * kKeys + lg * box_rows;
+                    int row = it.q0 + pos;
+                    if (a.kv.table && lg < boxes) {
+                        row = none;                                    // past the cache: zero fill
+                        if (pos < it.n_kv) {
+                            const int64_t c = cache_row(a.kv.table + (int64_t)it.n * a.kv.max_pages, pos, a.kv.page_shift,
+                                                        a.kv.n_pages);
+                            if (c >= 0)
+                                row = (int)c;
+                            else
+                                atomicMax(&g_attn_tc_error, GDN_DEVERR_PAGE);
+                        }
+                    }
+                    if (t >= S) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], (uint32_t)((t / S) & 1) ^ 1u));
+                    if (!ok) break;
+                    if (lane == 0) tc::mbar_expect_tx(&kv_full[s], C::kTile);
+                    __syncwarp();
+                    if (lg < boxes)
+                        tc::tma_load_3d(ring + s * C::kTile + lh * C::kHalf + lg * box_rows * 128, is_v ? &tv : &tk,
+                                        &kv_full[s], lh * 64, it.kvh, row);
                 }
-                // (no arrival that nobody waits for: it could land after the block has left)
-                for (int t = 2 * i + 1; ok && t <= 2 * i + (have_k ? 2 : 1); ++t)
-                    if (t + C::kRing < 2 * it.total) tc::mma_commit(&kv_empty[t % C::kRing]);
             }
-            if (!ok) {
-                s_timeout = 1;
-                tc::mma_commit(&drain);
-                tc::mbar_wait(&drain, 0);
+            if (!ok) {       // an expired wait: give the copies under way time to land
+                if (lane == 0) s_timeout = 1;
+                for (int i = 0; i < S; ++i) tc::mbar_wait(&kv_full[i], (uint32_t)(((t - 1 - i) / S) & 1), 1000000);
             }
+        } else if (warp < 10) {
+            // ---- products of tile x ---------------------------------------------------------
+            // (the whole warp walks the loop, one elected lane issues)
+            const int x = warp - 8;
+            const uint32_t neg = a.scale < 0.f ? 1u << 13 : 0u;        // -Q: scores of a negative scale
+            const uint32_t id_s = tc::idesc_bf16(128, kKeys, 0, 0) | neg, id_o = tc::idesc_bf16(128, D, 0, 1);
+            const uint64_t qd = tc::desc_sw128(tc::smem_u32(q_smem + x * C::kTile), 0, 1024);
+            const uint64_t kd = tc::desc_sw128(tc::smem_u32(ring), 0, 1024), vd = tc::desc_sw128(tc::smem_u32(ring), C::kHalf, 1024);
+            bool ok = true;
+            int t0 = 0, items = 0, mine = 0, others = 0;               // ring tiles, items and steps before this item
+            int last = -1;                                             // the tile that used S last
+            auto wait = [&](uint64_t* bar, int phase) {
+                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, (uint32_t)phase & 1u));
+            };
+            auto wait_kv = [&](int t) { wait(&kv_full[t % S], t / S); };
+            Item it;
+            for (int r = 0; ok && item_at(a, plan, count, tokens, r, it); ++r) {
+                const int steps = it.steps(x), other = it.steps(x ^ 1), total = it.total();
+                if (total == 0) continue;
+                wait(&q_full, items);
+                ++items;
+                for (int i = -1; i < total && ok; ++i) {               // S(i + 1), then O += P(i) V(i)
+                    if (i + 1 < total) {
+                        const int t = i < 0 ? t0 : t0 + 2 * i + 1;     // ring tile of K(i + 1)
+                        wait_kv(t);
+                        if (i + 1 < steps) {
+                            // S is free once its last user has read it: the other tile's turn
+                            // between ours, or whichever came last
+                            if (!C::kOneS) {
+                                if (mine + i >= 0) wait(&s_read[x], mine + i);
+                            } else if (x == 0 ? i >= 0 && i < other : i + 1 < other) {
+                                wait(&s_read[x ^ 1], others + i + x);
+                            } else if (i >= 0) {
+                                wait(&s_read[x], mine + i);
+                            } else if (last >= 0) {
+                                wait(&s_read[last], (last == x ? mine : others) - 1);
+                            }
+                            tc::tc_fence_after();
+                            if (ok && tc::elect_one()) {
+                                const uint64_t k_off = (uint64_t)((t % S) * (C::kTile >> 4));
+#pragma unroll
+                                for (int k = 0; k < D / 16; ++k) {
+                                    const uint32_t off = ((k >> 2) * C::kHalf + (k & 3) * 32) >> 4;
+                                    tc::mma_bf16(tmem + C::s_col(x), qd + off, kd + k_off + off, id_s, k > 0);
+                                }
+                                tc::mma_commit(&s_full[x]);
+                                tc::mma_commit(&kv_empty[t % S]);
+                                if (i + 2 == steps) tc::mma_commit(&q_empty);
+                            }
+                        } else if (ok && lane == 0) {
+                            tc::mbar_arrive(&kv_empty[t % S]);         // a tile of keys that only the other tile takes
+                            if (i < 0) tc::mbar_arrive(&q_empty);
+                        }
+                        __syncwarp();
+                    }
+                    if (i < 0) continue;
+                    const int t = t0 + (i + 1 < total ? 2 * i + 2 : 2 * i + 1);       // ring tile of V(i)
+                    wait_kv(t);
+                    if (i < steps) {
+                        wait(&p_full[x], mine + i);
+                        tc::tc_fence_after();
+                        if (ok && tc::elect_one()) {
+                            const uint64_t v_off = (uint64_t)((t % S) * (C::kTile >> 4));
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; ++k)
+                                tc::mma_bf16_ts(tmem + C::o_col(x), tmem + C::p_col(x) + k * 8, vd + v_off + k * 128, id_o,
+                                                i > 0 || k > 0);
+                            tc::mma_commit(&pv_done[x]);
+                            tc::mma_commit(&kv_empty[t % S]);
+                        }
+                    } else if (ok && lane == 0) {
+                        tc::mbar_arrive(&kv_empty[t % S]);
+                    }
+                    __syncwarp();
+                }
+                t0 += 2 * total;
+                mine += steps;
+                others += other;
+                last = it.steps(1) == total ? 1 : 0;
+            }
+            // every arrival of the commits above has landed before the block leaves
+            if (tc::elect_one()) tc::mma_commit(&drain[x]);
+            __syncwarp();
+            if (!tc::mbar_wait(&drain[x], 0) || !ok) s_timeout = 1;
         }
-        __syncwarp();
-    }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
-        // ---- softmax: thread = row -------------------------------------------------------
+        // ---- softmax: thread = row ---------------------------------------------------------
         const int x = warp >> 2;
         const int row = (warp & 3) * 32 + lane;
-        const int steps = it.steps[x];
-        const int tok = row / G;
-        const bool live = tok < it.ntok[x];
-        // last key this row sees (idle rows: no mask; nothing of them is kept)
-        const int lim = live ? it.past + it.tok[x] + tok : INT32_MAX;
+        const int tok = row / G, g = row - tok * G;
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;         // TMEM lane 32 (warp % 4)
-        const uint32_t ts = tmem + lane_base + x * 128, to = tmem + lane_base + 256 + x * D;
+        const uint32_t ts = tmem + lane_base + C::s_col(x), tp = tmem + lane_base + C::p_col(x),
+                       to = tmem + lane_base + C::o_col(x);
         const float sc = fabsf(a.scale) * kLog2e;
-        // the tile that clears the values past the item's last key
-        const bool clears = x == (it.steps[0] == it.total ? 0 : 1);
-        const int kv_end = max(it.past + (it.ntok[1] > 0 ? it.tok[1] + it.ntok[1] : it.tok[0] + it.ntok[0]), 0);
-        float m = -INFINITY, l = 0.f;
-        bool ok = true, finite = true;
-        for (int i = 0; i < steps; ++i) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[x], (uint32_t)(i & 1)));
-            if (!ok) break;
-            tc::tc_fence_after();
-            float s[128];
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) tc::tmem_ld32_raw(ts + c, reinterpret_cast<uint32_t*>(s) + c);
-            tc::tmem_wait_ld();
-            const int j0 = i * kKeys;
-            const bool masked = __any_sync(0xffffffffu, j0 + kKeys - 1 > lim);
-            if (masked) {
-#pragma unroll
-                for (int j = 0; j < 128; ++j)
-                    if (j0 + j > lim) s[j] = -INFINITY;
-            }
-            float mx = max3(s[0], s[1], s[2]), mx2 = max3(s[3], s[4], s[5]);
-#pragma unroll
-            for (int j = 6; j < 126; j += 4) {
-                mx = max3(mx, s[j], s[j + 1]);
-                mx2 = max3(mx2, s[j + 2], s[j + 3]);
-            }
-            mx = max3(mx, s[126], s[127]);
-            mx = fmaxf(mx, mx2) * sc;
-            if (!(mx == mx)) mx = INFINITY;         // (-inf * 0: nothing seen, or scale 0 and infinite scores)
-            const bool none = lim < j0;              // no key of this step is seen: m and l stay
-            if (none) mx = -INFINITY;
-            const bool move = mx > m + kGrow || (m == -INFINITY && !none);
-            if (move && mx == -INFINITY) finite = false;      // every key seen so far scores -inf
-            if (__any_sync(0xffffffffu, move)) {
-                const float alpha = move && m != -INFINITY ? exp2_sfu(m - mx) : 1.f;
-                if (move) {
-                    l *= alpha;
-                    m = mx;
-                }
-                if (i > 0) {
-#pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tc::tmem_ld32_raw(to + c, o);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tc::tmem_st32_raw(to + c, o);
-                    }
-                }
-            }
-            const float base = m == -INFINITY ? 0.f : m;
-            const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int c = 0; c < 128; c += 64) {
-                uint32_t p[32];
-#pragma unroll
-                for (int j = 0; j < 64; j += 2) {
-                    float e0, e1;
-                    unpack2(fma2(pack2(s[c + j], s[c + j + 1]), sc2, nb2), e0, e1);
-                    if (masked) {                    // exact zeros where masked
-                        e0 = j0 + c + j > lim ? 0.f : exp2_sfu(e0);
-                        e1 = j0 + c + j + 1 > lim ? 0.f : exp2_sfu(e1);
-                    } else if ((j & 7) == 6) {
-                        exp2_poly(e0, e1);
-                    } else {
-                        e0 = exp2_sfu(e0);
-                        e1 = exp2_sfu(e1);
-                    }
-                    sum = add2(sum, pack2(e0, e1));
-                    p[j / 2] = pack_bf16(e0, e1);
-                }
-                tc::tmem_st32_raw(ts + c / 2, p);
-            }
-            float s0, s1;
-            unpack2(sum, s0, s1);
-            l += s0 + s1;
-            if (clears && i + 1 == it.total && kv_end - j0 < kKeys) {
-                // values that no row of the block sees may be anything: clear them
-                const int t = 2 * i + 1, slot = t % C::kRing;
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_full[slot], (uint32_t)((t / C::kRing) & 1)));
+        bool ok = true;
+        int t0 = 0, done = 0;                                          // ring tiles and steps before this item
+        Item it;
+        for (int r = 0; ok && item_at(a, plan, count, tokens, r, it); ++r) {
+            const int steps = it.steps(x), total = it.total();
+            // last key this row sees (idle rows: no mask; nothing of them is kept)
+            const int lim = tok < it.ntok(x) ? it.past + it.tok + x * tokens + tok : INT32_MAX;
+            // the tile that clears the values past the item's last key: the first such key
+            const int clear_from = x == (it.steps(0) == total ? 0 : 1) ? max(it.end(0), it.end(1)) : INT32_MAX;
+            float m = -INFINITY, l = 0.f;
+            bool finite = true;
+            for (int i = 0; i < steps; ++i) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[x], (uint32_t)(done + i) & 1u));
                 if (!ok) break;
-                uint8_t* v = ring + slot * C::kTile;
-                const int first = kv_end - j0;
-                for (int e = (warp & 3) * 32 + lane; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
-                    const int r = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
-                    *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                tc::tc_fence_after();
+                float s[128];
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) tc::tmem_ld32_raw(ts + c, reinterpret_cast<uint32_t*>(s) + c);
+                tc::tmem_wait_ld();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&s_read[x]);
+                const int j0 = i * kKeys;
+                const bool masked = __any_sync(0xffffffffu, j0 + kKeys - 1 > lim);
+                if (masked) {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j0 + j > lim) s[j] = -INFINITY;
                 }
-                tc::fence_async_smem();
+                float mx = max3(s[0], s[1], s[2]), mx1 = max3(s[3], s[4], s[5]), mx2 = max3(s[6], s[7], s[8]),
+                      mx3 = max3(s[9], s[10], s[11]);
+#pragma unroll
+                for (int j = 12; j < 124; j += 8) {
+                    mx = max3(mx, s[j], s[j + 1]);
+                    mx1 = max3(mx1, s[j + 2], s[j + 3]);
+                    mx2 = max3(mx2, s[j + 4], s[j + 5]);
+                    mx3 = max3(mx3, s[j + 6], s[j + 7]);
+                }
+                mx = max3(mx, s[124], s[125]);
+                mx1 = max3(mx1, s[126], s[127]);
+                mx = max3(mx, mx1, fmaxf(mx2, mx3)) * sc;
+                if (!(mx == mx)) mx = INFINITY;         // (-inf * 0: nothing seen, or scale 0 and infinite scores)
+                const bool none = lim < j0;              // no key of this step is seen: m and l stay
+                if (none) mx = -INFINITY;
+                const bool move = mx > m + kGrow || (m == -INFINITY && !none);
+                if (move && mx == -INFINITY) finite = false;      // every key seen so far scores -inf
+                if (__any_sync(0xffffffffu, move)) {
+                    const float alpha = move && m != -INFINITY ? exp2_sfu(m - mx) : 1.f;
+                    if (move) {
+                        l *= alpha;
+                        m = mx;
+                    }
+                    if (i > 0) {
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
+                        if (!ok) break;
+                        tc::tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 16) {
+                            float o[16];
+                            tc::tmem_ld16(to + c, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                            tc::tmem_st16_raw(to + c, reinterpret_cast<uint32_t*>(o));
+                        }
+                    }
+                }
+                if (clear_from - j0 < kKeys) {
+                    // values that no row of the block sees may be anything: clear them
+                    const int t = t0 + 2 * total - 1, slot = t % S;           // the item's last values
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_full[slot], (uint32_t)((t / S) & 1)));
+                    if (!ok) break;
+                    uint8_t* v = ring + slot * C::kTile;
+                    const int first = clear_from - j0;
+                    for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
+                        const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
+                        *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_async_smem();
+                }
+                const float base = m == -INFINITY ? 0.f : m;
+                auto free = [&] {                        // the last step's product has read P
+                    if (i > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
+                    tc::tc_fence_after();
+                };
+                if (masked)
+                    l += weights<true>(s, sc, base, lim - j0, tp, free);
+                else
+                    l += weights<false>(s, sc, base, 0, tp, free);
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (!ok) break;
+                if (lane == 0) tc::mbar_arrive(&p_full[x]);
             }
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&p_full[x]);
-        }
-        if (steps > 0 && ok) {
-            ok = __all_sync(0xffffffffu, tc::mbar_wait(&o_full[x], 0));
-            tc::tc_fence_after();
-        }
-        if (!ok && lane == 0) s_timeout = 1;
-        if (ok) {
-            const bool empty = lim < 0;
+            if (!ok) break;
+            if (steps > 0) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + steps - 1) & 1u));
+                if (!ok) break;
+                tc::tc_fence_after();
+            }
+            item_at(a, plan, count, tokens, r, it);       // (again: not kept in registers over the loop)
+            const bool live = tok < it.ntok(x), empty = lim < 0;
             const float inv = empty ? 0.f : 1.0f / l;
-            const int64_t at = (((int64_t)it.sq.q0 + it.tok[x] + tok) * a.HQ + it.kvh * G + (row - tok * G)) * D;
+            const int64_t at = (((int64_t)it.q0 + it.tok + x * tokens + tok) * a.HQ + it.kvh * G + g) * D;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -435,28 +519,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                                             pack_bf16(o[e * 8 + 4], o[e * 8 + 5]), pack_bf16(o[e * 8 + 6], o[e * 8 + 7]));
                 }
             }
-            if (!finite && live) s_redo = 1;
+            if (__any_sync(0xffffffffu, !finite && live) && lane == 0) {
+                // (rows of a bad table may be listed twice: never past the list's end)
+                const int k = atomicAdd(&plan.counts[1], 1);
+                if (k < plan.max_redo)
+                    plan.redo[k] = make_int4(it.n, it.kvh, (it.tok + x * tokens) * G + (warp & 3) * 32,
+                                             min(32, tokens * G - (warp & 3) * 32));
+            }
+            tc::tc_fence_before();       // the reads of O are over before the next item's weights are handed on
+            t0 += 2 * it.total();
+            done += steps;
         }
+        if (!ok && lane == 0) s_timeout = 1;
     }
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     if (warp == 8) tc::tmem_dealloc(tmem, 512);
-    if (tid == 0) {
-        if (s_timeout) atomicMax(&g_attn_tc_error, GDN_DEVERR_TIMEOUT);
-        // tiles of a bad table may be listed twice: never past the list's end
-        if (s_redo) {
-            const int at = atomicAdd(&plan.counts[1], 1);
-            if (at < plan.max_redo) plan.redo[at] = make_int4(pt.x, pt.y, it.kvh, 0);
-        }
-    }
+    if (tid == 0 && s_timeout) atomicMax(&g_attn_tc_error, GDN_DEVERR_TIMEOUT);
 }
 
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     using C = Cfg<D>;
     const int G = a.HQ / a.HKV, tokens = kRows / G;
-    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, a.HKV, 1, 2 * tokens);
+    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 8 * a.HKV, 1, 2 * tokens);
     cudaError_t e = launch_attn_plan(a, plan, 1, 2 * tokens, s);
     if (e != cudaSuccess) return e;
     CUtensorMap tq, tk, tv;
@@ -478,12 +565,16 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     e = cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    attn_prefill_kernel<D><<<(unsigned)(plan.max_tiles * a.HKV), kThreads, C::kSmem, s>>>(tq, tk, tv, a, plan, tokens,
-                                                                                         box_rows);
-    e = cudaGetLastError();
+    int dev = 0, sms = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int64_t most = (int64_t)plan.max_tiles * a.HKV;
+    e = launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), C::kSmem, s, tq, tk,
+                   tv, a, plan, tokens, box_rows);
     if (e != cudaSuccess) return e;
     count_launch();
-    return launch_attn_redo(a, plan, 2 * tokens, s);
+    return launch_attn_redo(a, plan, s);
 }
 
 }  // namespace
@@ -491,7 +582,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 bool attn_tc_supported(int HQ, int HKV) { return HQ / HKV <= kRows; }
 
 size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV) {
-    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, HKV, 1, 2 * (kRows / (HQ / HKV)));
+    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, 8 * HKV, 1, 2 * (kRows / (HQ / HKV)));
     return p.bytes;
 }
 
