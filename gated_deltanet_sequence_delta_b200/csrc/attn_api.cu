@@ -80,7 +80,7 @@ size_t prefill_bytes(int64_t n_tokens, int32_t n_seqs, int32_t HQ, int32_t HKV, 
     if (n_tokens < 0 || n_tokens > INT32_MAX || n_seqs < 0 || check_heads(io, HQ, HKV, D) != GDN_OK) return 0;
     // the kernels count tiles (of one token or more, per key-value head) in 32 bits
     if ((n_tokens + n_seqs) * (int64_t)HQ > INT32_MAX) return 0;
-    if (io == GDN_BF16 && gdn::attn_tc_supported(HQ, HKV)) return gdn::attn_tc_bytes(n_tokens, n_seqs, HQ, HKV);
+    if (io == GDN_BF16 && gdn::attn_tc_supported(HQ, HKV)) return gdn::attn_tc_bytes(n_tokens, n_seqs, HQ, HKV, D);
     return gdn::attn_cudacore_bytes(n_tokens, n_seqs, HQ, HKV);
 }
 
@@ -212,7 +212,7 @@ gdn_status gdn_attn_status(int32_t* device_error) {
     if (e != cudaSuccess) return cuda_status(e);
     int32_t word = 0;
     for (auto read : {gdn::read_append_error, gdn::read_attn_cudacore_error, gdn::read_attn_decode_error,
-                      gdn::read_attn_tc_error}) {
+                      gdn::read_attn_tc_error, gdn::read_attn_plan_error}) {
         int32_t w = 0;
         e = read(&w);
         if (e != cudaSuccess) return cuda_status(e);

@@ -54,20 +54,34 @@ __device__ __forceinline__ SeqRows seq_rows(const AttnArgs& a, int n) {
     return seq_rows(a.cu, a.kv.kv_lens, n, a.T, a.n_tokens, (int64_t)a.kv.max_pages << a.kv.page_shift);
 }
 
-// Scratch of the prompt attentions, built by the plan kernel and filled in by the main one:
-// word 0 the number of tiles, word 1 the number of records to redo, then {sequence, tile} pairs
-// (longest key range first), then {sequence, key-value head, first row, rows} records to redo
-// (rows of that head's (token, query head) rows of the sequence).
+// Scratch of the prompt attentions, built by the plan kernel and filled in by the main one.
+// A tile is the work of one key-value head on a run of a sequence's rows.
+struct PlanTile {
+    int n, index;               // sequence, which of its tiles
+    int q0, n_q, n_kv;          // the sequence's rows (seq_rows)
+    int steps;                  // key steps of 128 (kept by the tensor-core path), at least 1
+    int before;                 // steps of the tiles before it in the list (split plans only)
+    int pad;
+};
 struct AttnPlan {
-    int32_t* counts;
-    int2* tiles;
-    int4* redo;
+    int32_t* counts;            // [0] tiles, [1] records to redo, [3] blocks that share the steps evenly (a split
+                                // plan), or 0: whole tiles
+    PlanTile* tiles;            // longest key range first
+    int4* redo;                 // {sequence, key-value head, first row, rows} of that head's (token, query head) rows
+    float2* part_ml;            // pieces of tiles that blocks share: [block][2][256] (maximum, sum), and
+    float* part_o;              // [block][2][256][D]
     int max_tiles, max_redo;
+    bool can_split;
     size_t bytes;
 };
-// Tiles of `tile_rows` rows, `row_per_tok` rows a token; room for `redo` records a tile.
-AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows);
-cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s);
+constexpr int kSplitGrid = 160;     // blocks that a split plan has room for
+constexpr int kSplitRows = 256;
+// Tiles of `tile_rows` rows, `row_per_tok` rows a token; room for `redo` records a tile; split_heads > 0:
+// a plan that may split tiles between blocks, that many key-value heads to a tile.
+AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows, int split_heads,
+                   int D);
+cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, int grid,
+                             cudaStream_t s);
 
 // Launch with programmatic stream serialisation: the kernel may start while the one before it
 // drains, and waits in griddepcontrol.wait before it touches memory.
@@ -88,12 +102,20 @@ cudaError_t launch_pdl(void (*f)(P...), dim3 grid, dim3 block, size_t smem, cuda
 
 // out * sigmoid(z)
 __device__ __forceinline__ float gate_out(float o, float z) { return o / (1.0f + expf(-z)); }
+// The same for a result that is rounded to bf16: the special-function units' 2^x and reciprocal
+// (a few 2^-23 each, against the rounding's 2^-8) without the division's fix-up.
+__device__ __forceinline__ float gate_out_fast(float o, float z) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return o * r;
+}
 
 cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
 // bf16 on the tensor cores; the query heads of a group have to fit a tile's rows.
 bool attn_tc_supported(int HQ, int HKV);
-size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
+size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
 // Redo the rows that the plan lists, on CUDA cores.
 cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
@@ -106,5 +128,6 @@ cudaError_t read_append_error(int32_t* out);
 cudaError_t read_attn_cudacore_error(int32_t* out);
 cudaError_t read_attn_decode_error(int32_t* out);
 cudaError_t read_attn_tc_error(int32_t* out);
+cudaError_t read_attn_plan_error(int32_t* out);
 
 }  // namespace gdn

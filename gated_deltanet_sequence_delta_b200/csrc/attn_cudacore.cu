@@ -229,10 +229,10 @@ __global__ void __launch_bounds__(kThreads) attn_cc_kernel(AttnArgs a, AttnPlan 
     Smem<D>& sm = *reinterpret_cast<Smem<D>*>(smem_raw);
     tc::grid_dependency_sync();
     if ((int)blockIdx.x >= plan.counts[0]) return;
-    const int2 it = plan.tiles[blockIdx.x];
-    const SeqRows sq = seq_rows(a, it.x);
+    const PlanTile it = plan.tiles[blockIdx.x];
+    const SeqRows sq = {it.q0, it.n_q, it.n_kv, 0};
     const int G = a.HQ / a.HKV;
-    attn_tile<IO, D>(a, sm, sq, it.x, blockIdx.y, (int64_t)it.y * kM, G, blockIdx.y * G, (int64_t)sq.n_q * G);
+    attn_tile<IO, D>(a, sm, sq, it.n, blockIdx.y, (int64_t)it.index * kM, G, blockIdx.y * G, (int64_t)sq.n_q * G);
 }
 
 // The rows that the tensor-core kernel listed.
@@ -250,58 +250,6 @@ __global__ void __launch_bounds__(kThreads) attn_redo_kernel(AttnArgs a, AttnPla
     }
 }
 
-// The plan: every sequence's tiles, the longest key ranges first (the grid starts them in
-// order, so the short ones fill the end).  Counting sort over kBuckets lengths; the order
-// inside a bucket varies and changes no result.
-constexpr int kPlanThreads = 1024, kBuckets = 256;
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, AttnPlan plan, int per, int tile_rows) {
-    __shared__ int s_count[kBuckets];
-    __shared__ int s_max;
-    const int tid = threadIdx.x;
-    for (int i = tid; i < kBuckets; i += kPlanThreads) s_count[i] = 0;
-    if (tid == 0) s_max = 1;
-    __syncthreads();
-    tc::grid_dependency_sync();
-    int mx = 1;
-    for (int n = tid; n < a.n_seqs; n += kPlanThreads) {
-        const SeqRows r = seq_rows(a, n);
-        if (r.bad) atomicMax(&g_cc_error, r.bad);
-        mx = max(mx, r.n_kv);
-    }
-    atomicMax(&s_max, mx);
-    __syncthreads();
-    const int width = (s_max - 1) / kBuckets + 1;
-    auto bucket = [&](const SeqRows& r, int t) {
-        const int64_t last = min(((int64_t)t + 1) * tile_rows, (int64_t)r.n_q * per) - 1;
-        const int keys = max(r.n_kv - r.n_q + (int)(last / per), 0);
-        return kBuckets - 1 - min(keys / width, kBuckets - 1);
-    };
-    // a sequence per warp, a tile per lane
-    for (int pass = 0; pass < 2; ++pass) {
-        for (int n = tid >> 5; n < a.n_seqs; n += kPlanThreads / 32) {
-            const SeqRows r = seq_rows(a, n);
-            const int tiles = (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
-            for (int t = tid & 31; t < tiles; t += 32) {
-                const int at = atomicAdd(&s_count[bucket(r, t)], 1);
-                // sequences of a bad table may overlap: never past the list's end
-                if (pass == 1 && at < plan.max_tiles) plan.tiles[at] = make_int2(n, t);
-            }
-        }
-        __syncthreads();
-        if (pass == 0 && tid == 0) {
-            int sum = 0;
-            for (int i = 0; i < kBuckets; ++i) {
-                const int c = s_count[i];
-                s_count[i] = sum;
-                sum += c;
-            }
-            plan.counts[0] = min(sum, plan.max_tiles);
-            plan.counts[1] = 0;
-        }
-        __syncthreads();
-    }
-}
-
 template <typename IO, int D>
 cudaError_t launch_cc(const AttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
     cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<IO, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -314,28 +262,6 @@ cudaError_t launch_cc(const AttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
 }
 
 }  // namespace
-
-AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows) {
-    AttnPlan p;
-    const int64_t tiles = (n_tokens * row_per_tok + tile_rows - 1) / tile_rows + n_seqs;
-    uint8_t* b = static_cast<uint8_t*>(ws);
-    p.max_tiles = (int)tiles;
-    p.max_redo = (int)(tiles * redo);
-    p.counts = reinterpret_cast<int32_t*>(b);
-    size_t at = kStatusBytes;
-    p.tiles = reinterpret_cast<int2*>(b + at);
-    at += (size_t)((tiles * sizeof(int2) + 255) / 256 * 256);
-    p.redo = reinterpret_cast<int4*>(b + at);
-    at += (size_t)(((size_t)tiles * redo * sizeof(int4) + 255) / 256 * 256);
-    p.bytes = at;
-    return p;
-}
-
-cudaError_t launch_attn_plan(const AttnArgs& a, const AttnPlan& p, int row_per_tok, int tile_rows, cudaStream_t s) {
-    const cudaError_t e = launch_pdl(attn_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, a, p, row_per_tok, tile_rows);
-    if (e == cudaSuccess) count_launch();
-    return e;
-}
 
 cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     const size_t smem = a.D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>);
@@ -350,14 +276,14 @@ cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t 
 }
 
 size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV) {
-    return attn_plan(nullptr, n_tokens, n_seqs, 0, HQ / HKV, kM).bytes;
+    return attn_plan(nullptr, n_tokens, n_seqs, 0, HQ / HKV, kM, 0, 0).bytes;
 }
 
 cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s) {
     if (a.n_tokens == 0 || a.n_seqs == 0) return cudaSuccess;
     const int G = a.HQ / a.HKV;
-    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 0, G, kM);
-    cudaError_t e = launch_attn_plan(a, plan, G, kM, s);
+    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 0, G, kM, 0, 0);
+    cudaError_t e = launch_attn_plan(a, plan, G, kM, 0, s);
     if (e != cudaSuccess) return e;
     if (a.bf16) return a.D == 128 ? launch_cc<__nv_bfloat16, 128>(a, plan, s) : launch_cc<__nv_bfloat16, 64>(a, plan, s);
     return a.D == 128 ? launch_cc<float, 128>(a, plan, s) : launch_cc<float, 64>(a, plan, s);

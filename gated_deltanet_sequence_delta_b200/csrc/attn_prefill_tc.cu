@@ -51,6 +51,7 @@ constexpr int kThreads = 384;
 // keeps 72 (2 x 216 + 72 = 3 x 168).
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr int kRows = 128, kKeys = 128;
+constexpr int kItems = 4;                // work items known ahead
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGrow = 8.0f;            // growth of the maximum (log2) that moves the reference
 
@@ -62,6 +63,10 @@ struct Cfg {
     static constexpr int kRing = D == 128 ? 5 : 8;               // key / value tiles
     static constexpr int kSmem = (2 + kRing) * kTile + 1024;
     static constexpr bool kOneS = D == 128;                      // one S for both tiles
+    // An eighth of the exponentials on the FMA pipes pays where they bound the step (D = 64: 242
+    // against 255 us for 8K tokens, 16 heads over 4); at D = 128 it costs (3.48 against 3.43 ms for
+    // 32K tokens).
+    static constexpr bool kPoly = D == 64;
     // TMEM columns
     __device__ static constexpr int s_col(int x) { return kOneS ? 0 : x * 128; }
     __device__ static constexpr int p_col(int x) { return (kOneS ? 128 : 256) + x * 64; }
@@ -124,7 +129,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 // A row's weights 2^(s sc - base) as bf16 in tensor memory (keys 2j, 2j + 1 in column j); returns
 // their sum.  `free` is called before the first write.  MASKED: keys past `last` weigh exactly 0,
 // and all the others go through the special-function units (the cubic does not reach 0).
-template <bool MASKED, typename F>
+template <bool MASKED, bool POLY, typename F>
 __device__ __forceinline__ float weights(const float (&s)[128], float sc, float base, int last, uint32_t tp, F free) {
     const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
     uint64_t sum[4] = {0, 0, 0, 0};
@@ -138,7 +143,7 @@ __device__ __forceinline__ float weights(const float (&s)[128], float sc, float 
             if (MASKED) {
                 e0 = c + j > last ? 0.f : exp2_sfu(e0);
                 e1 = c + j + 1 > last ? 0.f : exp2_sfu(e1);
-            } else if ((j & 7) == 6) {
+            } else if (POLY && (j & 15) == 14) {
                 exp2_poly(e0, e1);
             } else {
                 e0 = exp2_sfu(e0);
@@ -155,33 +160,31 @@ __device__ __forceinline__ float weights(const float (&s)[128], float sc, float 
     return a + b;
 }
 
-// One item of a block's work: tiles A and B of a (sequence, tile pair, key-value head).
+// One item of a block's work: tiles A and B of a (sequence, tile pair, key-value head), or the
+// steps s0 .. s1 - 1 of it.
 struct Item {
-    int n, kvh, q0, n_q, n_kv, past;
+    int n, kvh, q0, n_q, n_kv;
     int tok;                   // first token of A; B follows `tokens` later
-    int tokens;
-    // of tile x: tokens it has (0: no tile), keys its last row sees, steps of 128 keys
-    __device__ __forceinline__ int ntok(int x) const { return max(min(tokens, n_q - tok - x * tokens), 0); }
-    __device__ __forceinline__ int end(int x) const { return ntok(x) > 0 ? max(past + tok + x * tokens + ntok(x), 0) : 0; }
-    __device__ __forceinline__ int steps(int x) const { return (end(x) + kKeys - 1) / kKeys; }
-    __device__ __forceinline__ int total() const { return max(steps(0), steps(1)); }
+    int s0, s1;
+    int slot;                  // where a piece's sums go, -1: the item is whole; -2: no more items
+    __device__ __forceinline__ int past() const { return n_kv - n_q; }
+    // of tile x: tokens it has (0: no tile), keys its last row sees, steps of 128 keys of this item
+    __device__ __forceinline__ int ntok(int x, int tokens) const { return max(min(tokens, n_q - tok - x * tokens), 0); }
+    __device__ __forceinline__ int end(int x, int tokens) const {
+        const int k = ntok(x, tokens);
+        return k > 0 ? max(past() + tok + x * tokens + k, 0) : 0;
+    }
+    __device__ __forceinline__ int steps(int x, int tokens) const {
+        return max(min((end(x, tokens) + kKeys - 1) / kKeys, s1) - s0, 0);
+    }
+    __device__ __forceinline__ int total(int tokens) const { return max(steps(0, tokens), steps(1, tokens)); }
+    __device__ __forceinline__ int first(int tokens) const { return steps(0, tokens) > 0 ? 0 : 1; }   // tile of its first step
 };
-// The r-th item of this block.  The list runs from long to short; blocks take it forwards and
-// backwards in turn, which evens out their sums.
-__device__ __forceinline__ bool item_at(const AttnArgs& a, const AttnPlan& plan, int count, int tokens, int r, Item& it) {
-    const int64_t i = (int64_t)r * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-    if (i >= count) return false;
-    const int2 pt = plan.tiles[i / a.HKV];
-    const SeqRows sq = seq_rows(a, pt.x);
-    it.n = pt.x;
-    it.kvh = (int)(i % a.HKV);
-    it.q0 = sq.q0;
-    it.n_q = sq.n_q;
-    it.n_kv = sq.n_kv;
-    it.past = sq.n_kv - sq.n_q;
-    it.tok = pt.y * 2 * tokens;
-    it.tokens = tokens;
-    return true;
+
+// (Rows of a bad table may be listed twice: never past the list's end.)
+__device__ __forceinline__ void list_redo(const AttnPlan& plan, int n, int kvh, int row, int rows) {
+    const int k = atomicAdd(&plan.counts[1], 1);
+    if (k < plan.max_redo) plan.redo[k] = make_int4(n, kvh, row, rows);
 }
 
 template <int D>
@@ -192,8 +195,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     using C = Cfg<D>;
     constexpr int S = C::kRing;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], s_read[2], p_full[2], pv_done[2],
-        drain[2];
+    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], turn[2], p_full[2], pv_done[2],
+        v_last[2], drain[2], item_full[kItems], item_empty[kItems];
+    __shared__ Item s_item[kItems];
     __shared__ uint32_t s_tmem;
     __shared__ int s_timeout;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -210,9 +214,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         }
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(&s_full[x], 1);
-            tc::mbar_init(&s_read[x], 4);
+            tc::mbar_init(&turn[x], 4);
             tc::mbar_init(&p_full[x], 4);
             tc::mbar_init(&pv_done[x], 1);
+            tc::mbar_init(&v_last[x], 1);
+        }
+        for (int i = 0; i < kItems; ++i) {
+            tc::mbar_init(&item_full[i], 1);
+            tc::mbar_init(&item_empty[i], 11);
         }
         tc::mbar_init(&drain[0], 1);
         tc::mbar_init(&drain[1], 1);
@@ -228,7 +237,19 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     tc::tc_fence_after();
     const uint32_t tmem = s_tmem;
     tc::grid_dependency_sync();          // the plan is ready, and what ran before has left o alone
-    const int count = plan.counts[0] * a.HKV;
+
+    // the item ring's reader side: item r, or slot -2 past the last one (or after an expired wait)
+    auto item_at = [&](int r, bool& ok) {
+        Item it;
+        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&item_full[r % kItems], (uint32_t)(r / kItems) & 1u));
+        it = s_item[r % kItems];
+        if (!ok) it.slot = -2;
+        return it;
+    };
+    auto item_done = [&](int r) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&item_empty[r % kItems]);
+    };
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
@@ -239,9 +260,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const int lg = lane / C::kHalves, lh = lane % C::kHalves;  // this lane's box, its column block
             const int none = (int)((int64_t)a.kv.n_pages << a.kv.page_shift);
             int t = 0, items = 0;
-            Item it;
-            for (int r = 0; ok && item_at(a, plan, count, tokens, r, it); ++r) {
-                const int total = it.total();
+            for (int r = 0; ok; ++r) {
+                const Item it = item_at(r, ok);
+                item_done(r);
+                if (it.slot == -2) break;
+                const int total = it.total(tokens);
                 for (int u = 0; u < 2 * total; ++u, ++t) {             // K_0, (Q), K_1, V_0, K_2, V_1, ..., V_last
                     const bool is_v = u + 1 == 2 * total || (u > 0 && (u & 1) == 0);
                     const int step = u + 1 == 2 * total ? total - 1 : is_v ? (u >> 1) - 1 : (u + 1) >> 1;
@@ -249,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         if (items > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty, (uint32_t)(items - 1) & 1u));
                         if (!ok) break;
                         if (lane == 0) {
-                            const int tiles = it.ntok(1) > 0 ? 2 : 1;
+                            const int tiles = it.ntok(1, tokens) > 0 ? 2 : 1;
                             tc::mbar_expect_tx(&q_full, (uint32_t)(tiles * C::kHalves * tokens * G * 128));
                             for (int x = 0; x < tiles; ++x)
                                 for (int h = 0; h < C::kHalves; ++h)
@@ -260,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         ++items;
                     }
                     const int s = t % S;
-                    const int pos = step * kKeys + lg * box_rows;
+                    const int pos = (it.s0 + step) * kKeys + lg * box_rows;
                     int row = it.q0 + pos;
                     if (a.kv.table && lg < boxes) {
                         row = none;                                    // past the cache: zero fill
@@ -295,16 +318,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const uint64_t qd = tc::desc_sw128(tc::smem_u32(q_smem + x * C::kTile), 0, 1024);
             const uint64_t kd = tc::desc_sw128(tc::smem_u32(ring), 0, 1024), vd = tc::desc_sw128(tc::smem_u32(ring), C::kHalf, 1024);
             bool ok = true;
-            int t0 = 0, items = 0, mine = 0, others = 0;               // ring tiles, items and steps before this item
-            int last = -1;                                             // the tile that used S last
+            int t0 = 0, items = 0, mine = 0;                           // ring tiles, items and steps before this item
+            int turns = -1;                                            // phases of turn[x] taken
             auto wait = [&](uint64_t* bar, int phase) {
                 if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, (uint32_t)phase & 1u));
             };
             auto wait_kv = [&](int t) { wait(&kv_full[t % S], t / S); };
-            Item it;
-            for (int r = 0; ok && item_at(a, plan, count, tokens, r, it); ++r) {
-                const int steps = it.steps(x), other = it.steps(x ^ 1), total = it.total();
-                if (total == 0) continue;
+            for (int r = 0; ok; ++r) {
+                const Item it = item_at(r, ok);
+                item_done(r);
+                if (it.slot == -2) break;
+                const int steps = it.steps(x, tokens), total = it.total(tokens);
+                if (items == 0 && C::kOneS && it.first(tokens) != x) turns = 0;
                 wait(&q_full, items);
                 ++items;
                 for (int i = -1; i < total && ok; ++i) {               // S(i + 1), then O += P(i) V(i)
@@ -312,17 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         const int t = i < 0 ? t0 : t0 + 2 * i + 1;     // ring tile of K(i + 1)
                         wait_kv(t);
                         if (i + 1 < steps) {
-                            // S is free once its last user has read it: the other tile's turn
-                            // between ours, or whichever came last
-                            if (!C::kOneS) {
-                                if (mine + i >= 0) wait(&s_read[x], mine + i);
-                            } else if (x == 0 ? i >= 0 && i < other : i + 1 < other) {
-                                wait(&s_read[x ^ 1], others + i + x);
-                            } else if (i >= 0) {
-                                wait(&s_read[x], mine + i);
-                            } else if (last >= 0) {
-                                wait(&s_read[last], (last == x ? mine : others) - 1);
-                            }
+                            // S is ours once its last user has read it (the first time it is free)
+                            if (turns >= 0) wait(&turn[x], turns);
+                            ++turns;
                             tc::tc_fence_after();
                             if (ok && tc::elect_one()) {
                                 const uint64_t k_off = (uint64_t)((t % S) * (C::kTile >> 4));
@@ -341,10 +358,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         }
                         __syncwarp();
                     }
-                    if (i < 0) continue;
                     const int t = t0 + (i + 1 < total ? 2 * i + 2 : 2 * i + 1);       // ring tile of V(i)
-                    wait_kv(t);
-                    if (i < steps) {
+                    if (i >= 0) wait_kv(t);
+                    if (i >= 0 && i < steps) {
+                        if (i + 1 == total && ok && lane == 0) tc::mbar_arrive(&v_last[x]);
+                        __syncwarp();
                         wait(&p_full[x], mine + i);
                         tc::tc_fence_after();
                         if (ok && tc::elect_one()) {
@@ -356,20 +374,78 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             tc::mma_commit(&pv_done[x]);
                             tc::mma_commit(&kv_empty[t % S]);
                         }
-                    } else if (ok && lane == 0) {
+                    } else if (i >= 0 && ok && lane == 0) {
                         tc::mbar_arrive(&kv_empty[t % S]);
                     }
                     __syncwarp();
                 }
                 t0 += 2 * total;
                 mine += steps;
-                others += other;
-                last = it.steps(1) == total ? 1 : 0;
             }
             // every arrival of the commits above has landed before the block leaves
             if (tc::elect_one()) tc::mma_commit(&drain[x]);
             __syncwarp();
             if (!tc::mbar_wait(&drain[x], 0) || !ok) s_timeout = 1;
+        } else {
+            // ---- items: read ahead of the roles, so that no one waits for the list -------------------
+            const int tiles = plan.counts[0], shared = plan.counts[3];
+            bool ok = true;
+            int r = 0;
+            auto put = [&](const Item& it) {
+                if (it.slot != -2 && it.total(tokens) == 0) {
+                    // no row of the tile sees a key: the CUDA-core kernel writes its zeros
+                    for (int row = lane * 64; row < 2 * tokens * G; row += 32 * 64)
+                        list_redo(plan, it.n, it.kvh, it.tok * G + row, min(64, 2 * tokens * G - row));
+                    return;
+                }
+                if (r >= kItems) ok = __all_sync(0xffffffffu, tc::mbar_wait(&item_empty[r % kItems], (uint32_t)(r / kItems - 1) & 1u));
+                if (ok && lane == 0) {
+                    s_item[r % kItems] = it;
+                    tc::mbar_arrive(&item_full[r % kItems]);
+                }
+                __syncwarp();
+                ++r;
+            };
+            Item it = {};
+            if (shared == 0) {
+                // whole tiles: the list runs from long to short; blocks take it forwards and
+                // backwards in turn, which evens out their sums
+                const int64_t count = (int64_t)tiles * a.HKV;
+                for (int j = 0; ok; ++j) {
+                    const int64_t i = (int64_t)j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                    if (i >= count) break;
+                    const PlanTile t = plan.tiles[i / a.HKV];
+                    put(Item{t.n, (int)(i % a.HKV), t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, 0, t.steps, -1});
+                }
+            } else if ((int)blockIdx.x < shared) {
+                // an even share of all steps, tile by tile, key-value head by key-value head
+                const PlanTile end = plan.tiles[tiles - 1];
+                const int64_t N = (int64_t)(end.before + end.steps) * a.HKV;
+                int64_t at = N * blockIdx.x / shared;
+                const int64_t stop = N * (blockIdx.x + 1) / shared;
+                int k = 0;                                         // the tile that holds step `at`
+                for (int b = 0; b < tiles; b += 32) {
+                    const bool in = b + lane < tiles && (int64_t)plan.tiles[b + lane].before * a.HKV <= at;
+                    const unsigned m = __ballot_sync(0xffffffffu, in);
+                    if (m) k = b + 31 - __clz(m);
+                }
+                for (; ok && at < stop; ++k) {
+                    const PlanTile t = plan.tiles[k];
+                    int64_t o = at - (int64_t)t.before * a.HKV;
+                    for (int h = (int)(o / t.steps); ok && h < a.HKV && at < stop; ++h) {
+                        const int s0 = (int)(o - (int64_t)h * t.steps);
+                        const int s1 = (int)min((int64_t)t.steps, s0 + stop - at);
+                        const bool whole = s0 == 0 && s1 == t.steps;
+                        put(Item{t.n, h, t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, s0, s1,
+                                    whole ? -1 : (int)blockIdx.x * 2 + (s0 == 0 ? 1 : 0)});
+                        at += s1 - s0;
+                        o += s1 - s0;
+                    }
+                }
+            }
+            it.slot = -2;
+            if (ok) put(it);
+            if (!ok && lane == 0) s_timeout = 1;
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -382,14 +458,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                        to = tmem + lane_base + C::o_col(x);
         const float sc = fabsf(a.scale) * kLog2e;
         bool ok = true;
-        int t0 = 0, done = 0;                                          // ring tiles and steps before this item
-        Item it;
-        for (int r = 0; ok && item_at(a, plan, count, tokens, r, it); ++r) {
-            const int steps = it.steps(x), total = it.total();
-            // last key this row sees (idle rows: no mask; nothing of them is kept)
-            const int lim = tok < it.ntok(x) ? it.past + it.tok + x * tokens + tok : INT32_MAX;
+        int t0 = 0, done = 0, lasts = 0;                               // ring tiles, steps and last steps before this item
+        for (int r = 0; ok; ++r) {
+            Item it = item_at(r, ok);
+            if (it.slot == -2) break;
+            const int steps = it.steps(x, tokens), other = it.steps(x ^ 1, tokens), total = max(steps, other);
+            // last key this row sees (idle rows: no mask; nothing of them is kept); keys are
+            // counted from the item's first step
+            const int first_key = it.s0 * kKeys;
+            const int lim = tok < it.ntok(x, tokens) ? it.past() + it.tok + x * tokens + tok - first_key : INT32_MAX;
             // the tile that clears the values past the item's last key: the first such key
-            const int clear_from = x == (it.steps(0) == total ? 0 : 1) ? max(it.end(0), it.end(1)) : INT32_MAX;
+            const int clear_from = x == (it.steps(0, tokens) == total ? 0 : 1)
+                                       ? max(it.end(0, tokens), it.end(1, tokens)) - first_key : INT32_MAX;
             float m = -INFINITY, l = 0.f;
             bool finite = true;
             for (int i = 0; i < steps; ++i) {
@@ -402,7 +482,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 tc::tmem_wait_ld();
                 tc::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(&s_read[x]);
+                // S goes to the tile whose step comes next, A(0) B(0) A(1) ...: each MMA warp waits for
+                // every phase of its own barrier, one a turn
+                int next = x;
+                if (C::kOneS) {
+                    const bool them = x == 0 ? i < other : i + 1 < other;
+                    next = them ? x ^ 1 : x;
+                    if (!them && i + 1 == steps) {
+                        const Item after = item_at(r + 1, ok);
+                        next = after.slot == -2 ? -1 : after.first(tokens);
+                    }
+                }
+                if (lane == 0 && next >= 0) tc::mbar_arrive(&turn[next]);
                 const int j0 = i * kKeys;
                 const bool masked = __any_sync(0xffffffffu, j0 + kKeys - 1 > lim);
                 if (masked) {
@@ -450,8 +541,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 }
                 if (clear_from - j0 < kKeys) {
                     // values that no row of the block sees may be anything: clear them
-                    const int t = t0 + 2 * total - 1, slot = t % S;           // the item's last values
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_full[slot], (uint32_t)((t / S) & 1)));
+                    // (the MMA warp, which sees every copy land in turn, tells when they are there)
+                    const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&v_last[x], (uint32_t)lasts & 1u));
                     if (!ok) break;
                     uint8_t* v = ring + slot * C::kTile;
                     const int first = clear_from - j0;
@@ -467,9 +559,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     tc::tc_fence_after();
                 };
                 if (masked)
-                    l += weights<true>(s, sc, base, lim - j0, tp, free);
+                    l += weights<true, C::kPoly>(s, sc, base, lim - j0, tp, free);
                 else
-                    l += weights<false>(s, sc, base, 0, tp, free);
+                    l += weights<false, C::kPoly>(s, sc, base, 0, tp, free);
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
@@ -477,58 +569,85 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (lane == 0) tc::mbar_arrive(&p_full[x]);
             }
             if (!ok) break;
+            it = s_item[r % kItems];                      // (again: not kept in registers over the loop)
+            item_done(r);
+            const bool live = tok < it.ntok(x, tokens);
+            const int64_t at = (((int64_t)it.q0 + it.tok + x * tokens + tok) * a.HQ + it.kvh * G + g) * D;
+            // the gate's inputs, on their way while the last product runs
+            uint4 z[D / 8];
+            const bool gated = a.z && live && it.slot < 0;
+            if (gated) {
+#pragma unroll
+                for (int e = 0; e < D / 8; ++e) z[e] = reinterpret_cast<const uint4*>((const bf16*)a.z + at)[e];
+            }
             if (steps > 0) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + steps - 1) & 1u));
                 if (!ok) break;
                 tc::tc_fence_after();
             }
-            item_at(a, plan, count, tokens, r, it);       // (again: not kept in registers over the loop)
-            const bool live = tok < it.ntok(x), empty = lim < 0;
-            const float inv = empty ? 0.f : 1.0f / l;
-            const int64_t at = (((int64_t)it.q0 + it.tok + x * tokens + tok) * a.HQ + it.kvh * G + g) * D;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                float o[32];
+            if (it.slot >= 0) {
+                // a piece: the sums as they are, for the join
+                const int64_t pr = (int64_t)it.slot * kSplitRows + x * kRows + row;
+                if (live) plan.part_ml[pr] = make_float2(m, l);
                 if (steps > 0) {
-                    tc::tmem_ld32_raw(to + c, reinterpret_cast<uint32_t*>(o));
-                    tc::tmem_wait_ld();
-                }
-                if (live) {
+                    float4* out = reinterpret_cast<float4*>(plan.part_o + pr * D);
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 16) {
+                        float o[16];
+                        tc::tmem_ld16(to + c, o);
+                        tc::tmem_wait_ld();
+                        if (live) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        o[e] = empty ? 0.f : o[e] * inv;
-                        finite = finite && fabsf(o[e]) <= 3.4028235e38f;
-                    }
-                    if (a.z && !empty) {
-                        const uint4* z = reinterpret_cast<const uint4*>((const bf16*)a.z + at + c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint4 zz = z[e];
-                            const uint32_t w[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                o[e * 8 + 2 * k] = gate_out(o[e * 8 + 2 * k], __uint_as_float(w[k] << 16));
-                                o[e * 8 + 2 * k + 1] = gate_out(o[e * 8 + 2 * k + 1], __uint_as_float(w[k] & 0xffff0000u));
-                            }
+                            for (int e = 0; e < 4; ++e)
+                                out[c / 4 + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     }
-                    uint4* out = reinterpret_cast<uint4*>((bf16*)a.o + at + c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        out[e] = make_uint4(pack_bf16(o[e * 8], o[e * 8 + 1]), pack_bf16(o[e * 8 + 2], o[e * 8 + 3]),
-                                            pack_bf16(o[e * 8 + 4], o[e * 8 + 5]), pack_bf16(o[e * 8 + 6], o[e * 8 + 7]));
                 }
-            }
-            if (__any_sync(0xffffffffu, !finite && live) && lane == 0) {
-                // (rows of a bad table may be listed twice: never past the list's end)
-                const int k = atomicAdd(&plan.counts[1], 1);
-                if (k < plan.max_redo)
-                    plan.redo[k] = make_int4(it.n, it.kvh, (it.tok + x * tokens) * G + (warp & 3) * 32,
-                                             min(32, tokens * G - (warp & 3) * 32));
+            } else {
+                const bool empty = lim < 0;
+                const float inv = empty ? 0.f : 1.0f / l;
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    if (steps > 0) {
+                        tc::tmem_ld32_raw(to + c, reinterpret_cast<uint32_t*>(o));
+                        tc::tmem_wait_ld();
+                    }
+                    if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            o[e] = empty ? 0.f : o[e] * inv;
+                            finite = finite && fabsf(o[e]) <= 3.4028235e38f;
+                        }
+                        if (gated && !empty) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const uint4 zz = z[c / 8 + e];
+                                const uint32_t w[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int j = e * 8 + 2 * k;
+                                    o[j] = gate_out_fast(o[j], __uint_as_float(w[k] << 16));
+                                    o[j + 1] = gate_out_fast(o[j + 1], __uint_as_float(w[k] & 0xffff0000u));
+                                }
+                            }
+                        }
+                        uint4* out = reinterpret_cast<uint4*>((bf16*)a.o + at + c);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            out[e] = make_uint4(pack_bf16(o[e * 8], o[e * 8 + 1]), pack_bf16(o[e * 8 + 2], o[e * 8 + 3]),
+                                                pack_bf16(o[e * 8 + 4], o[e * 8 + 5]),
+                                                pack_bf16(o[e * 8 + 6], o[e * 8 + 7]));
+                    }
+                }
+                if (__any_sync(0xffffffffu, !finite && live) && lane == 0)
+                    list_redo(plan, it.n, it.kvh, (it.tok + x * tokens) * G + (warp & 3) * 32,
+                              min(32, tokens * G - (warp & 3) * 32));
             }
             tc::tc_fence_before();       // the reads of O are over before the next item's weights are handed on
-            t0 += 2 * it.total();
+            t0 += 2 * it.total(tokens);
             done += steps;
+            lasts += steps > 0 && steps == it.total(tokens);
         }
         if (!ok && lane == 0) s_timeout = 1;
     }
@@ -539,12 +658,83 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     if (tid == 0 && s_timeout) atomicMax(&g_attn_tc_error, GDN_DEVERR_TIMEOUT);
 }
 
+// Joins the pieces of a split plan.  Block (c, y): if block c of the main kernel began inside a
+// tile's steps, and is the first that did, rows 32 y .. 32 y + 31 of that tile.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a, AttnPlan plan, int tokens) {
+    constexpr int E = D / 32;
+    tc::grid_dependency_sync();
+    const int shared = plan.counts[3], tiles = plan.counts[0], c = blockIdx.x + 1;
+    if (c >= shared || tiles == 0) return;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const PlanTile end = plan.tiles[tiles - 1];
+    const int64_t N = (int64_t)(end.before + end.steps) * a.HKV;
+    auto start = [&](int b) { return N * b / shared; };
+    const int64_t at = start(c);
+    int k = 0;
+    for (int b = 0; b < tiles; b += 32) {
+        const bool in = b + lane < tiles && (int64_t)plan.tiles[b + lane].before * a.HKV <= at;
+        const unsigned m = __ballot_sync(0xffffffffu, in);
+        if (m) k = b + 31 - __clz(m);
+    }
+    const PlanTile t = plan.tiles[k];
+    const int h = (int)((at - (int64_t)t.before * a.HKV) / t.steps);
+    const int64_t t0 = (int64_t)t.before * a.HKV + (int64_t)h * t.steps, t1 = t0 + t.steps;
+    // the tile's blocks: the first is the last one that begins at or before t0 (no block is empty:
+    // there are at least as many steps as blocks)
+    const int c0 = (int)(((t0 + 1) * shared - 1) / N), c1 = (int)((t1 * shared - 1) / N);
+    if (at == t0 || c != c0 + 1) return;
+    const int G = a.HQ / a.HKV;
+    bool finite = true;
+    const int r0 = blockIdx.y * 32;
+    for (int r = r0 + w; r < r0 + 32; r += kJoinThreads / 32) {
+        const int x = r / kRows, tr = r - x * kRows, tok = t.index * 2 * tokens + x * tokens + tr / G;
+        if (tr >= tokens * G || tok >= t.n_q) continue;
+        const int lim = t.n_kv - t.n_q + tok;
+        float m = -INFINITY, l = 0.f, o[E] = {};
+        auto piece = [&](int b) { return ((int64_t)b * 2 + (b == c0 ? 1 : 0)) * kSplitRows + r; };
+        for (int b = c0; b <= c1; ++b) m = fmaxf(m, plan.part_ml[piece(b)].x);
+        const float base = m == -INFINITY ? 0.f : m;
+        for (int b = c0; b <= c1; ++b) {
+            const float2 ml = plan.part_ml[piece(b)];
+            // a piece in which the row sees no key has no sums
+            const int s0 = b == c0 ? 0 : (int)(start(b) - t0);
+            if (lim < s0 * kKeys) continue;
+            float f;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(ml.x - base));
+            l = fmaf(f, ml.y, l);
+            const float* p = plan.part_o + piece(b) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e], o[e]);
+        }
+        const int64_t to = (((int64_t)t.q0 + tok) * a.HQ + h * G + tr % G) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            float y = lim < 0 ? 0.f : o[e] / l;
+            finite = finite && fabsf(y) <= 3.4028235e38f;
+            if (a.z && lim >= 0) y = gate_out_fast(y, __bfloat162float(((const bf16*)a.z)[to + e]));
+            ((bf16*)a.o)[to + e] = __float2bfloat16_rn(y);
+        }
+    }
+    // (rows of the tile are listed as the (token, head) rows of the sequence)
+    if (__syncthreads_or(!finite) && tid == 0) {
+        const int x = r0 / kRows, tr = r0 - x * kRows;
+        list_redo(plan, t.n, h, (t.index * 2 + x) * tokens * G + tr, min(32, tokens * G - tr));
+    }
+}
+
 template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     using C = Cfg<D>;
     const int G = a.HQ / a.HKV, tokens = kRows / G;
-    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 8 * a.HKV, 1, 2 * tokens);
-    cudaError_t e = launch_attn_plan(a, plan, 1, 2 * tokens, s);
+    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 8 * a.HKV, 1, 2 * tokens, a.HKV, D);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int blocks = sms < kSplitGrid ? sms : kSplitGrid;
+    e = launch_attn_plan(a, plan, 1, 2 * tokens, blocks, s);
     if (e != cudaSuccess) return e;
     CUtensorMap tq, tk, tv;
     const int page = 1 << a.kv.page_shift;
@@ -565,15 +755,19 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         return cudaErrorInvalidValue;
     e = cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    int dev = 0, sms = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
+    // (a plan that may split is for the whole grid, however few its tiles)
     const int64_t most = (int64_t)plan.max_tiles * a.HKV;
-    e = launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)(most < sms ? most : sms)), dim3(kThreads), C::kSmem, s, tq, tk,
+    const int grid = plan.can_split || most > blocks ? blocks : (int)most;
+    e = launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tq, tk,
                    tv, a, plan, tokens, box_rows);
     if (e != cudaSuccess) return e;
     count_launch();
+    if (plan.can_split && grid > 1) {
+        e = launch_pdl(attn_join_rows_kernel<D>, dim3((unsigned)(grid - 1), kSplitRows / 32), dim3(kJoinThreads), 0, s, a,
+                       plan, tokens);
+        if (e != cudaSuccess) return e;
+        count_launch();
+    }
     return launch_attn_redo(a, plan, s);
 }
 
@@ -581,8 +775,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 
 bool attn_tc_supported(int HQ, int HKV) { return HQ / HKV <= kRows; }
 
-size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV) {
-    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, 8 * HKV, 1, 2 * (kRows / (HQ / HKV)));
+size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D) {
+    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, 8 * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
     return p.bytes;
 }
 

@@ -300,6 +300,53 @@ def test_prefill_nonfinite_in_masked_places(dtype, bad):
     assert G.gdn_attn_status() == 0
 
 
+@pytest.mark.parametrize("D,HQ,HKV", [(128, 8, 2), (128, 4, 4), (64, 8, 2), (128, 6, 2)])
+def test_prefill_back_to_back(D, HQ, HKV):
+    """Many launches with no gap between them, over lengths at which a block's two tiles take
+    different numbers of key steps: every one the same bits, no wait that runs out."""
+    torch, G = _torch()
+    g = _gen(16)
+    lens = [2100, 130, 70, 1, 900, 257, 33, 1500]
+    T, cu = sum(lens), _cu(lens)
+    q, k, v = _draw(g, (1, T, HQ, D), "bf16"), _draw(g, (1, T, HKV, D), "bf16"), _draw(g, (1, T, HKV, D), "bf16")
+    cud = _i32(cu)
+    outs = [torch.empty_like(q) for _ in range(60)]
+    ws = torch.empty(G.attn_prefill_workspace_bytes(T, len(lens), HQ, HKV, D, 1), dtype=torch.uint8, device="cuda")
+    for o in outs:
+        G.gdn_attn_prefill(q, k, v, cu_seqlens=cud, o=o, workspace=ws)
+    assert G.gdn_attn_status() == 0
+    for i, o in enumerate(outs):
+        assert torch.equal(o, outs[0]), i
+    kn, vn = _np(k[0]), _np(v[0])
+    for i in (0, 5):
+        a, b = cu[i], cu[i + 1]
+        _check_rows(outs[-1][0, a:b], q[0, a:b], kn[a:b], vn[a:b], 0, D ** -0.5, "bf16", None, f"sequence {i}",
+                    _some(lens[i], i, 10))
+
+
+def test_paged_back_to_back_split():
+    """The same for a few rows over long pasts, whose key ranges are shared between blocks."""
+    torch, G = _torch()
+    g = _gen(17)
+    new, past = [20, 3, 1, 64, 33, 40], [7000, 130, 12000, 2500, 9001, 3000]
+    totals = [n + p for n, p in zip(new, past)]
+    c = Cache(totals, 8, 128, 16, "bf16", 18)
+    q = _draw(g, (sum(new), 32, 128), "bf16")
+    z = _draw(g, q.shape, "bf16")
+    cud = _i32(_cu(new))
+    outs = [torch.empty_like(q) for _ in range(200)]
+    for o in outs:
+        G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cud, z=z, o=o)
+    assert G.gdn_attn_status() == 0
+    for i, o in enumerate(outs):
+        assert torch.equal(o, outs[0]), i
+    for i, n in enumerate(new):
+        kn, vn = c.seq(i)
+        a = _cu(new)[i]
+        _check_rows(o[a:a + n], q[a:a + n], kn, vn, past[i], 128 ** -0.5, "bf16", z[a:a + n], f"sequence {i}",
+                    sorted({0, n // 2, n - 1}))
+
+
 # ---- prompt pieces over the cache -----------------------------------------------------
 PAGED = [
     # dtype, D, HQ, HKV, page, new, past, gate
