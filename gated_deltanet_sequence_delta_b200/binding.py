@@ -513,47 +513,70 @@ def gdn_decode_status() -> int:
 
 
 # ---------------------------------------------------------------------------
-# The attention layers: a paged key-value cache and the attentions that read it.
-def _same_device(ref: torch.Tensor, *ts):
-    for t in ts:
-        if t is not None and t.device != ref.device:
-            raise ValueError(f"tensors on {ref.device} and {t.device}")
+# The attention layers: a paged key-value cache and the attentions that read it.  A decode step
+# calls these once a layer, so the marshalling is kept short: device, layout and address of a
+# tensor in one place, the raw stream of the tensors' own device.
+def _addr(t: torch.Tensor | None, dev: int):
+    """Address of a contiguous tensor on CUDA device `dev`, None for None."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors on one device")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    return t.data_ptr()
 
 
-def _int32(*ts):
-    for t in ts:
-        if t is not None and t.dtype != torch.int32:
-            raise TypeError("cu_seqlens, kv_lens and block_table must be int32")
+def _int32_addr(t: torch.Tensor | None, dev: int):
+    if t is not None and t.dtype is not torch.int32:
+        raise TypeError("cu_seqlens, kv_lens and block_table must be int32")
+    return _addr(t, dev)
+
+
+def _call_on(dev: int, fn, *args) -> int:
+    """fn(*args, current stream of device `dev`) with `dev` current."""
+    if dev == torch.cuda.current_device():
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+
+
+def _cuda_index(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be CUDA tensors")
+    return dev
 
 
 def _cache_sizes(k_cache, v_cache, block_table, kv_lens, dtype):
     """(n_pages, page_size, HKV, D, n_seqs, max_pages) of a paged cache, checked."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache, v_cache must be [n_pages, page_size, HKV, D]")
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise TypeError("the cache must have the dtype of the new tokens")
-    if block_table.dim() != 2 or kv_lens.shape != (block_table.shape[0],):
+    table = block_table.shape
+    if len(table) != 2 or kv_lens.shape != table[:1]:
         raise ValueError("block_table must be [n_seqs, max_pages] and kv_lens [n_seqs]")
-    _int32(block_table, kv_lens)
-    return (*k_cache.shape, *block_table.shape)
+    return (*shape, *table)
 
 
-def _token_stride(t: torch.Tensor) -> int:
+def _token_stride(t: torch.Tensor, dev: int) -> int:
     """Elements between the tokens of [tokens, heads, D], heads contiguous within a token."""
-    if not t.is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    D = t.shape[2]
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    if t.get_device() != dev:
+        raise ValueError("tensors must be CUDA tensors on one device")
+    n, H, D = t.shape
+    st = t.stride()
+    if st[2] != 1 or (H > 1 and st[1] != D):
         raise ValueError("a token's heads must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    return st[0] if n > 1 else H * D
 
 
-def _attn_ws(workspace, need: int, what: str, device):
-    if need == 0:
-        _check(4, what)
-    if workspace is None or workspace.numel() * workspace.element_size() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    return workspace, workspace.numel() * workspace.element_size()
+def _attn_ws(workspace, dev: int, query, *sizes):
+    """(tensor, address, bytes) of the caller's workspace, or of a new one of the size the query gives."""
+    if workspace is None:
+        workspace = torch.empty(int(query(*sizes)), dtype=torch.uint8, device=torch.device("cuda", dev))
+    return workspace, _addr(workspace, dev), workspace.numel() * workspace.element_size()
 
 
 def attn_prefill_workspace_bytes(n_tokens, n_seqs, HQ, HKV, D, io_dtype) -> int:
@@ -573,45 +596,44 @@ def gdn_attn_append(q, k, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens=
     [rotary_dim / 2], or None for no rotation.  Returns the rotated queries q_out [T, HQ, D]
     (None if q is None); q_out may be q."""
     T, HKV, D = k.shape
+    dev = _cuda_index(k)
     n_pages, page_size, cHKV, cD, N, max_pages = _cache_sizes(k_cache, v_cache, block_table, kv_lens, k.dtype)
-    if v.shape != k.shape or v.dtype != k.dtype or (cHKV, cD) != (HKV, D):
+    if v.shape != k.shape or v.dtype is not k.dtype or cHKV != HKV or cD != D:
         raise ValueError("k, v must be [T, HKV, D] of one dtype, with the cache's HKV and D")
-    HQ = HKV
+    HQ, q_ptr, q_stride = HKV, None, 0
     if q is not None:
         HQ = q.shape[1]
-        if q.shape != (T, HQ, D) or q.dtype != k.dtype:
+        if q.shape != (T, HQ, D) or q.dtype is not k.dtype:
             raise ValueError("q must be [T, HQ, D] with the dtype of k")
         if q_out is None:
             q_out = torch.empty((T, HQ, D), dtype=q.dtype, device=q.device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+        elif q_out.shape != q.shape or q_out.dtype is not q.dtype:
             raise ValueError("q_out must be shaped and typed like q")
+        q_ptr, q_stride = q.data_ptr(), _token_stride(q, dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     rotary = 0
     if inv_freq is not None:
-        if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+        if inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1:
             raise TypeError("inv_freq must be fp32 [rotary_dim / 2]")
         rotary = 2 * inv_freq.numel()
-    _int32(cu_seqlens)
     if cu_seqlens is not None and cu_seqlens.shape != (N + 1,):
         raise ValueError("cu_seqlens must be [n_seqs + 1]")
-    _same_device(k, q, v, k_cache, v_cache, block_table, kv_lens, cu_seqlens, inv_freq, q_out)
-    with torch.cuda.device(k.device):
-        st = lib().gdn_attn_append(
-            None if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(), _dtype_code(k),
-            0 if q is None else _token_stride(q), _token_stride(k), _token_stride(v), _ptr(inv_freq), rotary,
-            int(bool(interleaved)), _ptr(cu_seqlens), _ptr(kv_lens), _ptr(block_table), T, N, HQ, HKV, D, n_pages,
-            page_size, max_pages, _ptr(q_out), _ptr(k_cache), _ptr(v_cache), _stream())
-    _check(st, "gdn_attn_append")
+    st = _call_on(dev, lib().gdn_attn_append, q_ptr, k.data_ptr(), v.data_ptr(), _dtype_code(k), q_stride,
+                  _token_stride(k, dev), _token_stride(v, dev), _addr(inv_freq, dev), rotary, 1 if interleaved else 0,
+                  _int32_addr(cu_seqlens, dev), _int32_addr(kv_lens, dev), _int32_addr(block_table, dev), T, N, HQ, HKV,
+                  D, n_pages, page_size, max_pages, _addr(q_out, dev), _addr(k_cache, dev), _addr(v_cache, dev))
+    if st:
+        _check(st, "gdn_attn_append")
     return q_out
 
 
 def _attn_out(q, z, o):
-    if z is not None and (z.shape != q.shape or z.dtype != q.dtype):
+    if z is not None and (z.shape != q.shape or z.dtype is not q.dtype):
         raise ValueError("z must be shaped and typed like q")
     if o is None:
         return torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if o.shape != q.shape or o.dtype != q.dtype:
+    if o.shape != q.shape or o.dtype is not q.dtype:
         raise ValueError("o must be shaped and typed like q")
     return o
 
@@ -621,22 +643,22 @@ def gdn_attn_prefill(q, k, v, cu_seqlens=None, scale: float | None = None, z=Non
     and cu_seqlens int32 [N + 1]); scale defaults to 1 / sqrt(D); z like q gates the output by
     sigmoid(z).  Returns o like q."""
     B, T, HQ, D = q.shape
+    dev = _cuda_index(q)
     HKV = k.shape[2]
     if k.shape != (B, T, HKV, D) or v.shape != k.shape:
         raise ValueError("inconsistent q/k/v shapes")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
+    if k.dtype is not q.dtype or v.dtype is not q.dtype:
         raise TypeError("q, k, v must share one dtype")
-    _int32(cu_seqlens)
     N = cu_seqlens.numel() - 1 if cu_seqlens is not None else B
     o = _attn_out(q, z, o)
-    _same_device(q, k, v, cu_seqlens, z, o, workspace)
-    need = attn_prefill_workspace_bytes(B * T, N, HQ, HKV, D, _dtype_code(q))
-    with torch.cuda.device(q.device):
-        workspace, nws = _attn_ws(workspace, need, "gdn_attn_prefill", q.device)
-        st = lib().gdn_attn_prefill(_ptr(q), _ptr(k), _ptr(v), _dtype_code(q), _ptr(cu_seqlens), B, T, N, HQ, HKV, D,
-                                    D ** -0.5 if scale is None else float(scale), _ptr(z), _ptr(o), _ptr(workspace),
-                                    nws, _stream())
-    _check(st, "gdn_attn_prefill")
+    io = _dtype_code(q)
+    L = lib()
+    workspace, ws, nws = _attn_ws(workspace, dev, L.gdn_attn_prefill_workspace_bytes, B * T, N, HQ, HKV, D, io)
+    st = _call_on(dev, L.gdn_attn_prefill, _addr(q, dev), _addr(k, dev), _addr(v, dev), io,
+                  _int32_addr(cu_seqlens, dev), B, T, N, HQ, HKV, D, D ** -0.5 if scale is None else scale,
+                  _addr(z, dev), _addr(o, dev), ws, nws)
+    if st:
+        _check(st, "gdn_attn_prefill")
     return o
 
 
@@ -646,20 +668,20 @@ def gdn_attn_prefill_paged(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens
     packed by cu_seqlens int32 [N + 1]; cache, block_table and kv_lens as gdn_attn_append;
     scale and z as gdn_attn_prefill.  Returns o like q."""
     T, HQ, D = q.shape
+    dev = _cuda_index(q)
     n_pages, page_size, HKV, cD, N, max_pages = _cache_sizes(k_cache, v_cache, block_table, kv_lens, q.dtype)
     if cD != D or cu_seqlens.shape != (N + 1,):
         raise ValueError("the cache must have q's head dim, and cu_seqlens must be [n_seqs + 1]")
-    _int32(cu_seqlens)
     o = _attn_out(q, z, o)
-    _same_device(q, k_cache, v_cache, block_table, kv_lens, cu_seqlens, z, o, workspace)
-    need = attn_prefill_workspace_bytes(T, N, HQ, HKV, D, _dtype_code(q))
-    with torch.cuda.device(q.device):
-        workspace, nws = _attn_ws(workspace, need, "gdn_attn_prefill_paged", q.device)
-        st = lib().gdn_attn_prefill_paged(_ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                          _ptr(kv_lens), _ptr(cu_seqlens), T, N, HQ, HKV, D, n_pages, page_size,
-                                          max_pages, D ** -0.5 if scale is None else float(scale), _ptr(z), _ptr(o),
-                                          _ptr(workspace), nws, _stream())
-    _check(st, "gdn_attn_prefill_paged")
+    io = _dtype_code(q)
+    L = lib()
+    workspace, ws, nws = _attn_ws(workspace, dev, L.gdn_attn_prefill_workspace_bytes, T, N, HQ, HKV, D, io)
+    st = _call_on(dev, L.gdn_attn_prefill_paged, _addr(q, dev), io, _addr(k_cache, dev), _addr(v_cache, dev),
+                  _int32_addr(block_table, dev), _int32_addr(kv_lens, dev), _int32_addr(cu_seqlens, dev), T, N, HQ, HKV,
+                  D, n_pages, page_size, max_pages, D ** -0.5 if scale is None else scale, _addr(z, dev),
+                  _addr(o, dev), ws, nws)
+    if st:
+        _check(st, "gdn_attn_prefill_paged")
     return o
 
 
@@ -669,19 +691,19 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, kv_lens, scale: float | No
     max_pages] and kv_lens [B] as gdn_attn_append; scale and z as gdn_attn_prefill.  Returns o
     like q."""
     B, HQ, D = q.shape
+    dev = _cuda_index(q)
     n_pages, page_size, HKV, cD, N, max_pages = _cache_sizes(k_cache, v_cache, block_table, kv_lens, q.dtype)
     if cD != D or N != B:
         raise ValueError("the cache must have q's head dim, and block_table one row per sequence")
     o = _attn_out(q, z, o)
-    _same_device(q, k_cache, v_cache, block_table, kv_lens, z, o, workspace)
-    need = attn_decode_workspace_bytes(B, HQ, HKV, D, _dtype_code(q))
-    with torch.cuda.device(q.device):
-        workspace, nws = _attn_ws(workspace, need, "gdn_attn_decode", q.device)
-        st = lib().gdn_attn_decode(_ptr(q), _dtype_code(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                   _ptr(kv_lens), B, HQ, HKV, D, n_pages, page_size, max_pages,
-                                   D ** -0.5 if scale is None else float(scale), _ptr(z), _ptr(o), _ptr(workspace),
-                                   nws, _stream())
-    _check(st, "gdn_attn_decode")
+    io = _dtype_code(q)
+    L = lib()
+    workspace, ws, nws = _attn_ws(workspace, dev, L.gdn_attn_decode_workspace_bytes, B, HQ, HKV, D, io)
+    st = _call_on(dev, L.gdn_attn_decode, _addr(q, dev), io, _addr(k_cache, dev), _addr(v_cache, dev),
+                  _int32_addr(block_table, dev), _int32_addr(kv_lens, dev), B, HQ, HKV, D, n_pages, page_size,
+                  max_pages, D ** -0.5 if scale is None else scale, _addr(z, dev), _addr(o, dev), ws, nws)
+    if st:
+        _check(st, "gdn_attn_decode")
     return o
 
 

@@ -1,6 +1,8 @@
 // attn_common.cuh -- declarations shared by the attention kernels' .cu files.
 #pragma once
 
+#include <atomic>
+
 #include "gdn_internal.cuh"
 #include "paged.cuh"
 
@@ -98,6 +100,19 @@ cudaError_t launch_pdl(void (*f)(P...), dim3 grid, dim3 block, size_t smem, cuda
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, f, args...);
+}
+
+// Let a kernel use `bytes` of dynamic shared memory, once per device (`done`, a bit a device, is
+// the kernel's own): the call costs as much as a third of a launch.
+inline cudaError_t allow_smem(const void* f, size_t bytes, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // out * sigmoid(z)

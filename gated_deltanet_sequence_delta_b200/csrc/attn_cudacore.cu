@@ -252,8 +252,8 @@ __global__ void __launch_bounds__(kThreads) attn_redo_kernel(AttnArgs a, AttnPla
 
 template <typename IO, int D>
 cudaError_t launch_cc(const AttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
-    cudaError_t e = cudaFuncSetAttribute(attn_cc_kernel<IO, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)sizeof(Smem<D>));
+    static std::atomic<uint64_t> done{0};
+    cudaError_t e = allow_smem((const void*)attn_cc_kernel<IO, D>, sizeof(Smem<D>), done);
     if (e != cudaSuccess) return e;
     e = launch_pdl(attn_cc_kernel<IO, D>, dim3((unsigned)plan.max_tiles, (unsigned)a.HKV), dim3(kThreads),
                    sizeof(Smem<D>), s, a, plan);
@@ -266,7 +266,8 @@ cudaError_t launch_cc(const AttnArgs& a, const AttnPlan& plan, cudaStream_t s) {
 cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t s) {
     const size_t smem = a.D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>);
     const auto f = a.D == 128 ? attn_redo_kernel<128> : attn_redo_kernel<64>;
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<uint64_t> done[2];
+    cudaError_t e = allow_smem((const void*)f, smem, done[a.D == 128]);
     if (e != cudaSuccess) return e;
     // the list is empty unless something is not finite: a grid that starts and ends in about the
     // launch's own time, and still spreads a list over the device

@@ -40,8 +40,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 // R: query heads a block serves at once (rows of the statistics).
 template <typename IO, int D, int R>
 struct Cfg {
-    static constexpr int KT = sizeof(IO) == 2 ? 64 : 32;            // keys per tile
-    static constexpr int KW = KT / kTeamWarps;                      // keys per warp: 16 or 8
+    static constexpr int KT = sizeof(IO) == 2 || D == 64 ? 64 : 32; // keys per tile
+    static constexpr int KW = KT / kTeamWarps;                      // keys per warp: 16, or 8 (fp32, D = 128)
     static constexpr int NB = D * (int)sizeof(IO) / 128;            // 128-byte column blocks
     static constexpr int kBlk = KT * 128;                           // bytes of one column block
     static constexpr int kStage = 2 * NB * kBlk;                    // keys, then values
@@ -60,18 +60,19 @@ __device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, int kt, int* b
     return (r.n_kv + kt - 1) / kt;
 }
 
-// Block-wide: the total of per(n) over all sequences, and the sequence that holds unit `at` of
-// the concatenation with the units before it (n = -1: `at` is past the end).
+// Block-wide: the total of per(n) over all sequences, the blocks that share it (no more than there
+// are units, so that none is empty), and the sequence that holds block c's first unit with the
+// units before it (n = -1: block c has none).
 struct Place {
-    int64_t total, before;
-    int n;
+    int64_t total, before, at;
+    int n, blocks;
 };
 template <typename F>
-__device__ Place find_place(int n_seqs, F per, int64_t num, int64_t den, int64_t* at, int64_t* s_warp, Place* s_out) {
-    // thread t owns the sequences [t c, (t + 1) c)
+__device__ Place find_place(int n_seqs, F per, int c, int grid, int64_t* s_warp, Place* s_out) {
+    // thread t owns the sequences [t k, (t + 1) k)
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, nw = blockDim.x >> 5;
-    const int c = (n_seqs + blockDim.x - 1) / blockDim.x;
-    const int lo = min(tid * c, n_seqs), hi = min(lo + c, n_seqs);
+    const int k = (n_seqs + blockDim.x - 1) / blockDim.x;
+    const int lo = min(tid * k, n_seqs), hi = min(lo + k, n_seqs);
     int64_t sum = 0;
     for (int n = lo; n < hi; ++n) sum += per(n);
     int64_t incl = sum;
@@ -88,22 +89,25 @@ __device__ Place find_place(int n_seqs, F per, int64_t num, int64_t den, int64_t
         if (i < w) base += s_warp[i];
         total += s_warp[i];
     }
-    *at = total * num / den;
+    const int blocks = (int)min((int64_t)grid, total);
+    const int64_t at = c < blocks ? total * c / blocks : total;
     int64_t before = base + incl - sum;
-    if (*at >= before && *at < before + sum) {
+    if (at >= before && at < before + sum) {
         for (int n = lo; n < hi; ++n) {
-            const int64_t k = per(n);
-            if (*at < before + k) {
+            const int64_t u = per(n);
+            if (at < before + u) {
                 s_out->n = n;
                 s_out->before = before;
                 break;
             }
-            before += k;
+            before += u;
         }
     }
     __syncthreads();
     Place p = *s_out;
     p.total = total;
+    p.at = at;
+    p.blocks = blocks;
     return p;
 }
 
@@ -269,14 +273,16 @@ struct Warp<bf16, D, 16> {
     }
 };
 
-// fp32: a lane holds D / 32 columns of every row's output; the scores of key lane / 4 are
-// summed by its four lanes.
+// fp32: a lane holds D / 32 columns of every row's output; the scores of key 8 s + lane / 4 of the
+// warp's keys are summed by its four lanes.  The reference m moves only when a score exceeds it by
+// more than 2^8 (weights stay below that), so that a step usually needs no reduction over the
+// warp; l is a lane's own sum over its keys until the end.
 template <int D, int R>
 struct Warp<float, D, R> {
     using C = Cfg<float, D, R>;
-    static constexpr int E = D / 32;
+    static constexpr int E = D / 32, NS = C::KW / 8;
     float o[R][E];
-    float m[R], l[R];      // the same on every lane
+    float m[R], l[R];
 
     __device__ __forceinline__ void start(const float*, int, const float*) {
 #pragma unroll
@@ -291,50 +297,68 @@ struct Warp<float, D, R> {
     __device__ __forceinline__ void step(uint8_t* tile, int w, int valid, int rows, float sc, const float* sq) {
         const int lane = threadIdx.x & 31, key = lane >> 2, part = lane & 3;
         const uint8_t* vt = tile + C::NB * C::kBlk;
-        const int row = 8 * w + key;
-        float s[R];
+        float s[NS][R];
 #pragma unroll
-        for (int r = 0; r < R; ++r) s[r] = 0.f;
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int r = 0; r < R; ++r) s[n][r] = 0.f;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
             const int c = part + 4 * i;                       // 16-byte chunk of the row
-            const float4 k = *reinterpret_cast<const float4*>(tile + (c >> 3) * C::kBlk + row * 128 +
-                                                              (((c & 7) ^ (row & 7)) << 4));
+            float4 k[NS];
+#pragma unroll
+            for (int n = 0; n < NS; ++n)                      // (rows 8 apart: the same swizzle)
+                k[n] = *reinterpret_cast<const float4*>(tile + (c >> 3) * C::kBlk + (C::KW * w + 8 * n + key) * 128 +
+                                                        (((c & 7) ^ key) << 4));
 #pragma unroll
             for (int r = 0; r < R; ++r) {
                 const float4 q = *reinterpret_cast<const float4*>(sq + r * D + 4 * c);
-                s[r] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, s[r]))));
+#pragma unroll
+                for (int n = 0; n < NS; ++n)
+                    s[n][r] = fmaf(k[n].x, q.x, fmaf(k[n].y, q.y, fmaf(k[n].z, q.z, fmaf(k[n].w, q.w, s[n][r]))));
+            }
+        }
+        bool grow = false;
+#pragma unroll
+        for (int n = 0; n < NS; ++n)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float y = s[n][r];
+                y += __shfl_xor_sync(0xffffffffu, y, 1);
+                y += __shfl_xor_sync(0xffffffffu, y, 2);
+                y = 8 * n + key < valid ? y * sc : -INFINITY;
+                grow = grow || y > m[r] + 8.f;
+                s[n][r] = y;
+            }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                float mx = s[0][r];
+                if constexpr (NS == 2) mx = fmaxf(mx, s[1][r]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                mx = fmaxf(mx, m[r]);
+                const float al = mx == -INFINITY ? 1.f : exp2f(m[r] - mx);
+                m[r] = mx;
+                l[r] *= al;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[r][e] *= al;
             }
         }
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 1);
-            s[r] += __shfl_xor_sync(0xffffffffu, s[r], 2);
-            s[r] = key < valid ? s[r] * sc : -INFINITY;
-            float mx = s[r];
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            mx = fmaxf(mx, m[r]);
-            const float base = mx == -INFINITY ? 0.f : mx;
-            const float al = exp2f(m[r] - base);
-            m[r] = mx;
-            s[r] = exp2f(s[r] - base);
-            float sum = s[r];
-            sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-            l[r] = fmaf(l[r], al, sum);
+        for (int n = 0; n < NS; ++n)
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[r][e] *= al;
-        }
+            for (int r = 0; r < R; ++r) {
+                s[n][r] = exp2f(s[n][r] - (m[r] == -INFINITY ? 0.f : m[r]));
+                l[r] += s[n][r];
+            }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < C::KW; ++j) {
             if (j < valid) {                   // values past the context never enter
-                const int vr = 8 * w + j;
                 float v[E];
                 const int c = lane * E / 4;    // this lane's columns: E consecutive floats
-                const uint8_t* p = vt + (c >> 3) * C::kBlk + vr * 128 + (((c & 7) ^ (vr & 7)) << 4);
+                const uint8_t* p = vt + (c >> 3) * C::kBlk + (C::KW * w + j) * 128 + (((c & 7) ^ (j & 7)) << 4);
                 if constexpr (E == 4) {
                     *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
                 } else {
@@ -342,7 +366,7 @@ struct Warp<float, D, R> {
                 }
 #pragma unroll
                 for (int r = 0; r < R; ++r) {
-                    const float pr = __shfl_sync(0xffffffffu, s[r], j * 4);
+                    const float pr = __shfl_sync(0xffffffffu, s[j >> 3][r], (j & 7) * 4);
 #pragma unroll
                     for (int e = 0; e < E; ++e) o[r][e] = fmaf(pr, v[e], o[r][e]);
                 }
@@ -353,13 +377,17 @@ struct Warp<float, D, R> {
     __device__ __forceinline__ void put(float* out, int rows) {
         const int lane = threadIdx.x & 31;
 #pragma unroll
-        for (int r = 0; r < R; ++r)
+        for (int r = 0; r < R; ++r) {
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 4);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 8);
+            l[r] += __shfl_xor_sync(0xffffffffu, l[r], 16);
             if (r < rows) {
                 float* p = out + r * (D + 4);
 #pragma unroll
                 for (int e = 0; e < E; ++e) p[lane * E + e] = o[r][e];
                 if (lane == 0) *reinterpret_cast<float2*>(p + D) = make_float2(m[r], l[r]);
             }
+        }
     }
 };
 
@@ -415,13 +443,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     }
     tc::grid_dependency_sync();
     int bad = 0;
-    int64_t begin;
     const Place pl = find_place(
-        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, C::KT, &bad) * subs; }, blockIdx.x, gridDim.x, &begin,
-        s_warp, &s_place);
+        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, C::KT, &bad) * subs; }, blockIdx.x, gridDim.x, s_warp,
+        &s_place);
     if (bad && blockIdx.x == 0) atomicMax(&g_decode_attn_error, bad);
-    const int64_t end = pl.total * (blockIdx.x + 1) / gridDim.x;
-    const int64_t count = end - begin;
+    const int64_t begin = pl.at;
+    const int64_t count = pl.n < 0 ? 0 : pl.total * (blockIdx.x + 1) / pl.blocks - begin;
     // contexts of no keys: zeros, a sequence's rows by one block
     for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
         const SeqRows r = seq_rows(a, n);
@@ -576,60 +603,65 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
     __shared__ Place s_place;
     __shared__ float s_o[8][D];
     __shared__ float s_m[8], s_l[8];
-    tc::grid_dependency_sync();
     const int c = blockIdx.x + 1, r = blockIdx.y, tid = threadIdx.x;
     const int G = a.HQ / a.HKV, subs = a.HKV * hb;
     int bad = 0;
-    int64_t begin;
+    // (before the wait: the first kernel only lets this one start once what ran before it is over,
+    // so the lengths are there, and the first kernel does not write them)
     const Place pl = find_place(
-        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, KT, &bad) * subs; }, c, grid, &begin, s_warp, &s_place);
-    if (pl.n < 0) return;
-    const int tiles = tiles_of(a, pl.n, KT, &bad);
-    const int64_t in_seq = begin - pl.before;
-    const int sub = (int)(in_seq / tiles);
-    const int64_t t0 = pl.before + (int64_t)sub * tiles, t1 = t0 + tiles;
-    // blocks that hold tiles of [t0, t1): the first is the last one that begins at or before t0
-    const int64_t N = pl.total;
-    const int c0 = (int)(((t0 + 1) * grid - 1) / N), c1 = (int)((t1 * grid - 1) / N);
-    auto start = [&](int b) { return N * b / grid; };
-    if (begin == t0 || c0 == c1) return;
-    int first = c0 + 1;                       // the first block that begins inside the item
-    while (start(first) == start(first + 1)) ++first;      // (blocks of no tiles hold nothing)
-    if (c != first) return;
-    const int kvh = sub / hb, h0 = kvh * G + (sub - kvh * hb) * R;
-    if (h0 + r >= (kvh + 1) * G) return;
+        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, KT, &bad) * subs; }, c, grid, s_warp, &s_place);
+    int first = -1, last = 0, kvh = 0, h0 = 0;
+    if (pl.n >= 0) {
+        const int tiles = tiles_of(a, pl.n, KT, &bad);
+        const int sub = (int)((pl.at - pl.before) / tiles);
+        const int64_t t0 = pl.before + (int64_t)sub * tiles, N = pl.total;
+        // blocks that hold tiles of the item [t0, t0 + tiles): the first is the last one that begins
+        // at or before t0
+        const int c0 = (int)(((t0 + 1) * pl.blocks - 1) / N);
+        kvh = sub / hb;
+        h0 = kvh * G + (sub - kvh * hb) * R;
+        if (pl.at != t0 && c == c0 + 1 && h0 + r < (kvh + 1) * G) {
+            first = c0;
+            last = (int)(((t0 + tiles) * pl.blocks - 1) / N);
+        }
+    }
+    tc::grid_dependency_sync();
+    if (first < 0) return;
     const Partials part = partials(a.ws, R, D);
     const int w = tid >> 5, lane = tid & 31;
-    auto slot = [&](int b) { return ((int64_t)b * 2 + (b == c0 ? 1 : 0)) * R + r; };
-    float m = -INFINITY;
-    for (int b = c0 + w * 32 + lane; b <= c1; b += kJoinThreads)
-        if (start(b) != start(b + 1)) m = fmaxf(m, part.ml[slot(b)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) s_m[w] = m;
-    __syncthreads();
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, s_m[i]);
-    const float base = m == -INFINITY ? 0.f : m;
-    float l = 0.f, x[E] = {};
-#pragma unroll 4
-    for (int b = c0 + w; b <= c1; b += 8) {
-        if (start(b) == start(b + 1)) continue;
+    auto slot = [&](int b) { return ((int64_t)b * 2 + (b == first ? 1 : 0)) * R + r; };
+    // a warp every eighth piece, with its own running maximum
+    float m = -INFINITY, l = 0.f, x[E] = {};
+#pragma unroll 2
+    for (int b = first + w; b <= last; b += 8) {
         const float2 ml = part.ml[slot(b)];
-        const float f = exp2f(ml.x - base);
         const float* p = part.o + slot(b) * D + lane * E;
-        l = fmaf(f, ml.y, l);
+        float y[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(f, p[e], x[e]);
+        for (int e = 0; e < E; ++e) y[e] = p[e];
+        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(ml.x - base), g = exp2f(m - base);
+        m = mn;
+        l = fmaf(l, g, f * ml.y);
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], g, f * y[e]);
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = x[e];
-    if (lane == 0) s_l[w] = l;
+    if (lane == 0) {
+        s_m[w] = m;
+        s_l[w] = l;
+    }
     __syncthreads();
     if (tid < D) {
+        m = s_m[0];
+        for (int i = 1; i < 8; ++i) m = fmaxf(m, s_m[i]);
+        const float base = m == -INFINITY ? 0.f : m;
         float y = 0.f, sum = 0.f;
         for (int i = 0; i < 8; ++i) {
-            y += s_o[i][tid];
-            sum += s_l[i];
+            const float f = exp2f(s_m[i] - base);
+            y = fmaf(f, s_o[i][tid], y);
+            sum = fmaf(f, s_l[i], sum);
         }
         y /= sum;
         const int64_t at = ((int64_t)pl.n * a.HQ + h0 + r) * D + tid;
@@ -659,7 +691,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (!make_map(&tk, dt, a.kv.k, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&tv, dt, a.kv.v, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    e = cudaFuncSetAttribute(attn_decode_kernel<IO, D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem((const void*)attn_decode_kernel<IO, D, R>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     e = launch_pdl(attn_decode_kernel<IO, D, R>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tk, tv, a, hb);
     if (e != cudaSuccess) return e;

@@ -753,7 +753,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (!make_map(&tk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv.k, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map(&tv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.kv.v, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
-    e = cudaFuncSetAttribute(attn_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    static std::atomic<uint64_t> done{0};
+    e = allow_smem((const void*)attn_prefill_kernel<D>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     // (a plan that may split is for the whole grid, however few its tiles)
     const int64_t most = (int64_t)plan.max_tiles * a.HKV;

@@ -156,7 +156,7 @@ def test_append_refusals(L):
 
 def _prefill(L, **kw):
     a = dict(q=A, k=A + 16 * MB, v=A + 32 * MB, io=1, cu=None, B=2, T=100, N=2, HQ=8, HKV=2, D=128, scale=0.1, z=None,
-             o=A + 48 * MB, ws=A + 64 * MB, nws=MB)
+             o=A + 48 * MB, ws=A + 1024 * MB, nws=512 * MB)
     a.update(kw)
     return L.gdn_attn_prefill(a["q"], a["k"], a["v"], a["io"], a["cu"], a["B"], a["T"], a["N"], a["HQ"], a["HKV"],
                               a["D"], a["scale"], a["z"], a["o"], a["ws"], a["nws"], None)
@@ -180,8 +180,8 @@ def test_prefill_refusals(L):
 
 def _paged_call(L, **kw):
     a = dict(q=A, io=1, kc=A + 16 * MB, vc=A + 32 * MB, table=A + 100 * MB, lens=A + 101 * MB, cu=A + 102 * MB, T=100,
-             N=2, HQ=8, HKV=2, D=128, n_pages=64, page=16, width=20, scale=0.1, z=None, o=A + 48 * MB, ws=A + 64 * MB,
-             nws=MB)
+             N=2, HQ=8, HKV=2, D=128, n_pages=64, page=16, width=20, scale=0.1, z=None, o=A + 48 * MB, ws=A + 1024 * MB,
+             nws=512 * MB)
     a.update(kw)
     return L.gdn_attn_prefill_paged(a["q"], a["io"], a["kc"], a["vc"], a["table"], a["lens"], a["cu"], a["T"], a["N"],
                                     a["HQ"], a["HKV"], a["D"], a["n_pages"], a["page"], a["width"], a["scale"],
