@@ -17,8 +17,8 @@
 //
 // Block: a producer warp copies tiles into a ring in shared memory by TMA, 128B-swizzled, one
 // box per page part (rows of a token's head are 128 or 256 bytes, heads and tokens strided);
-// eight consumer warps in two teams take alternate tiles, a warp a fixed share of a tile's
-// keys, each with its own running statistics, so that teams only meet at the end of an item.
+// eight consumer warps in teams of two or four take the tiles in turn, a warp a fixed share of
+// a tile's keys, each with its own running statistics, so that teams only meet at the end of an item.
 //   bf16: mma.sync m16n8k16 with the group's heads as M (up to 16), the fragments read by
 //     ldmatrix; tcgen05 would need 128 rows and has nothing to gain on a tile read once.
 //   fp32: CUDA cores (no TF32), a lane a quarter of a key's elements for the scores, D / 32
@@ -33,31 +33,46 @@ using bf16 = __nv_bfloat16;
 
 __device__ int g_decode_attn_error;
 
-constexpr int kTeamWarps = 4, kConsumers = 8 * 32, kThreads = kConsumers + 32;
+constexpr int kWarps = 8, kConsumers = kWarps * 32, kThreads = kConsumers + 32;
 constexpr int kMaxGrid = 192;             // blocks, for the workspace size
 constexpr float kLog2e = 1.4426950408889634f;
 
 // R: query heads a block serves at once (rows of the statistics).
 template <typename IO, int D, int R>
 struct Cfg {
-    static constexpr int KT = sizeof(IO) == 2 || D == 64 ? 64 : 32; // keys per tile
-    static constexpr int KW = KT / kTeamWarps;                      // keys per warp: 16, or 8 (fp32, D = 128)
+    static constexpr int KT = 16384 / (D * (int)sizeof(IO));        // keys per tile: 32 KB of keys and values
+    static constexpr int TW = KT < 64 ? KT / 16 : 4;                // warps of a team, which share a tile
+    static constexpr int Teams = kWarps / TW;
+    static constexpr int KW = KT / TW;                              // keys per warp: 16, or 32 (bf16, D = 64)
     static constexpr int NB = D * (int)sizeof(IO) / 128;            // 128-byte column blocks
     static constexpr int kBlk = KT * 128;                           // bytes of one column block
     static constexpr int kStage = 2 * NB * kBlk;                    // keys, then values
     static constexpr int kMerge = 8 * R * (D + 4) * 4;              // the warps' outputs at an item's end
     static constexpr int kQ = sizeof(IO) == 4 ? R * D * 4 : 0;      // fp32: the rows' queries
     static constexpr int kFit = (226 * 1024 - 1024 - kMerge - kQ) / kStage;
-    // ring slots, an even number: a slot then always belongs to the same team, which waits for
-    // every phase of its barrier
-    static constexpr int kStages = kFit > 12 ? 12 : kFit / 2 * 2;
+    // ring slots, a multiple of the teams: a slot then always belongs to the same team, which waits
+    // for every phase of its barrier
+    static constexpr int kStages = kFit / Teams * Teams;
     static constexpr int kSmem = kStages * kStage + kMerge + kQ + 1024;
+    // What an item's start and end cost a block (its queries' way, the joining of its warps, about
+    // 2 us), in tiles.  It is counted in the split: 24 ragged contexts in fp32, 16 heads: 100 us
+    // without, 70 us with it.
+    static constexpr int kItemCost = 4;
 };
 
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, int kt, int* bad) {
     const SeqRows r = seq_rows(a, n);
     if (r.bad) *bad = r.bad;
     return (r.n_kv + kt - 1) / kt;
+}
+
+// Units of work of sequence n: per head (and row block) its tiles, one unit each, and in front of
+// them the item's cost.  Tile t of an item that begins at unit u is unit u + kItemCost + t; a block
+// has the tiles whose units are in its share.
+template <typename C>
+__device__ __forceinline__ int64_t cost_of(const AttnArgs& a, int n, int subs, int* bad) {
+    const int tiles = tiles_of(a, n, C::KT, bad);
+    return tiles > 0 ? (int64_t)(tiles + C::kItemCost) * subs : 0;
 }
 
 // Block-wide: the total of per(n) over all sequences, the blocks that share it (no more than there
@@ -112,12 +127,15 @@ __device__ Place find_place(int n_seqs, F per, int c, int grid, int64_t* s_warp,
 }
 
 struct Partials {
+    int4* desc;           // [grid]  {first, last block of the item that block c began inside, as the first that did,
+                          //          or first = -1; sequence; first query head}
     float* o;             // [grid][2][R][D]
     float2* ml;           // [grid][2][R]  (m in log2 units, l)
 };
 __host__ __device__ inline Partials partials(void* ws, int R, int D) {
     Partials p;
-    p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+    p.desc = reinterpret_cast<int4*>(static_cast<uint8_t*>(ws) + kStatusBytes);
+    p.ml = reinterpret_cast<float2*>(p.desc + kMaxGrid);
     p.o = reinterpret_cast<float*>(p.ml + kMaxGrid * 2 * R);
     return p;
 }
@@ -172,13 +190,14 @@ struct Warp<bf16, D, 16> {
         l[0] = l[1] = 0.f;
     }
 
-    // the warp's 16 keys, rows 16 w .. of the tile, of which the first `valid` exist (> 0)
+    // the warp's KW keys, rows KW w .. of the tile, of which the first `valid` exist (> 0)
     __device__ __forceinline__ void step(uint8_t* tile, int w, int valid, int, float sc, const float*) {
+        constexpr int NS = C::KW / 16;
         const int lane = threadIdx.x & 31;
         uint8_t* vt = tile + C::NB * C::kBlk;
-        if (valid < 16) {       // values past the context may be anything: 0 * NaN must not enter
-            for (int i = lane; i < (16 - valid) * C::NB * 8; i += 32) {
-                const int row = 16 * w + valid + i / (C::NB * 8), c = i % (C::NB * 8);
+        if (valid < C::KW) {    // values past the context may be anything: 0 * NaN must not enter
+            for (int i = lane; i < (C::KW - valid) * C::NB * 8; i += 32) {
+                const int row = C::KW * w + valid + i / (C::NB * 8), c = i % (C::NB * 8);
                 *reinterpret_cast<uint4*>(vt + (c >> 3) * C::kBlk + row * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
             }
             tc::fence_async_smem();        // before the ring slot's next copy overwrites them
@@ -186,39 +205,45 @@ struct Warp<bf16, D, 16> {
         }
         const uint32_t kb = tc::smem_u32(tile), vb = tc::smem_u32(vt);
         const int mat = lane >> 3, mr = lane & 7;
-        float s[2][4] = {};
+        float s[2 * NS][4] = {};
         {   // matrices: keys 0-7 and 8-15 (mat >> 1), element halves (mat & 1)
-            const int row = 16 * w + ((mat >> 1) << 3) + mr;
+            const int row = C::KW * w + ((mat >> 1) << 3) + mr;
             const uint32_t base = kb + row * 128;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                uint32_t b[4];
                 const int chunk = (k & 3) * 2 + (mat & 1);
-                ldsm4(base + (k >> 2) * C::kBlk + ((chunk ^ (row & 7)) << 4), b);
-                mma16816(s[0], q[k], b[0], b[1]);
-                mma16816(s[1], q[k], b[2], b[3]);
+                const uint32_t at = base + (k >> 2) * C::kBlk + ((chunk ^ mr) << 4);
+#pragma unroll
+                for (int n = 0; n < NS; ++n) {
+                    uint32_t b[4];
+                    ldsm4(at + n * 16 * 128, b);
+                    mma16816(s[2 * n], q[k], b[0], b[1]);
+                    mma16816(s[2 * n + 1], q[k], b[2], b[3]);
+                }
             }
         }
-        float mx[2] = {m[0], m[1]};
+        // the reference m moves only when a score exceeds it by more than 2^8 (weights stay below
+        // that), so that a step usually needs no reduction over the row's four threads
+        bool grow = false;
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = j * 8 + (lane & 3) * 2 + (i & 1);
                 s[j][i] = key < valid ? s[j][i] * sc : -INFINITY;
-                mx[i >> 1] = fmaxf(mx[i >> 1], s[j][i]);
+                grow = grow || s[j][i] > m[i >> 1] + 8.f;
             }
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 1));
-            mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xffffffffu, mx[r], 2));
-        }
-        if (__any_sync(0xffffffffu, mx[0] != m[0] || mx[1] != m[1])) {
+        if (__any_sync(0xffffffffu, grow)) {
             float al[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                al[r] = mx[r] == -INFINITY ? 1.f : exp2f(m[r] - mx[r]);
-                m[r] = mx[r];
+                float mx = m[r];
+#pragma unroll
+                for (int j = 0; j < 2 * NS; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * r], s[j][2 * r + 1]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                al[r] = mx == -INFINITY ? 1.f : exp2f(m[r] - mx);
+                m[r] = mx;
                 l[r] *= al[r];
             }
 #pragma unroll
@@ -231,23 +256,26 @@ struct Warp<bf16, D, 16> {
         }
         const float base[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 s[j][i] = exp2f(s[j][i] - base[i >> 1]);
                 l[i >> 1] += s[j][i];
             }
-        // the weights are rounded to bf16 for the product (half a step, 2^-8, each); their sum is not
-        const uint32_t p[4] = {pack_bf16(s[0][0], s[0][1]), pack_bf16(s[0][2], s[0][3]), pack_bf16(s[1][0], s[1][1]),
-                               pack_bf16(s[1][2], s[1][3])};
-        {   // matrices: keys 0-7 and 8-15 (mat & 1), column eights (mat >> 1)
-            const int row = 16 * w + ((mat & 1) << 3) + mr;
+#pragma unroll
+        for (int n = 0; n < NS; ++n) {
+            // the weights are rounded to bf16 for the product (half a step, 2^-8, each); their sum is not
+            const uint32_t p[4] = {pack_bf16(s[2 * n][0], s[2 * n][1]), pack_bf16(s[2 * n][2], s[2 * n][3]),
+                                   pack_bf16(s[2 * n + 1][0], s[2 * n + 1][1]),
+                                   pack_bf16(s[2 * n + 1][2], s[2 * n + 1][3])};
+            // matrices: keys 0-7 and 8-15 (mat & 1), column eights (mat >> 1)
+            const int row = C::KW * w + 16 * n + ((mat & 1) << 3) + mr;
             const uint32_t base_v = vb + row * 128;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c) {
                 uint32_t b[4];
                 const int chunk = (c & 3) * 2 + (mat >> 1);
-                ldsm4t(base_v + (c >> 2) * C::kBlk + ((chunk ^ (row & 7)) << 4), b);
+                ldsm4t(base_v + (c >> 2) * C::kBlk + ((chunk ^ mr) << 4), b);
                 mma16816(o[2 * c], p, b[0], b[1]);
                 mma16816(o[2 * c + 1], p, b[2], b[3]);
             }
@@ -391,28 +419,36 @@ struct Warp<float, D, R> {
     }
 };
 
-// Where a block is in its range: sequence, (head, row block) of it, tile of that item.
+// Where a block is in its share: sequence, (head, row block) of it, tile of that item, the tile's
+// unit.
 struct Cursor {
     int n, sub, tile, tiles, len;
+    int64_t unit;
 };
-__device__ __forceinline__ void cursor_load(const AttnArgs& a, Cursor& c, int kt) {
-    while (true) {      // the range ends before the sequences do, so one with tiles exists
+template <typename C>
+__device__ __forceinline__ void cursor_load(const AttnArgs& a, Cursor& c) {
+    while (true) {      // (the last sequence ends the search, tiles or not)
         const SeqRows r = seq_rows(a, c.n);
         c.len = r.n_kv;
-        c.tiles = (r.n_kv + kt - 1) / kt;
+        c.tiles = (r.n_kv + C::KT - 1) / C::KT;
         if (c.tiles > 0 || c.n + 1 >= a.n_seqs) return;
         ++c.n;
     }
 }
-__device__ __forceinline__ void cursor_next(const AttnArgs& a, Cursor& c, int kt, int subs, int64_t left) {
-    if (++c.tile < c.tiles) return;
+// To the next tile; false if it is not in the block's share, which ends before unit `end`.
+template <typename C>
+__device__ __forceinline__ bool cursor_next(const AttnArgs& a, Cursor& c, int subs, int64_t end) {
+    ++c.unit;
+    if (++c.tile < c.tiles) return c.unit < end;
+    c.unit += C::kItemCost;
+    if (c.unit >= end) return false;
     c.tile = 0;
-    if (++c.sub < subs) return;
-    c.sub = 0;
-    if (left > 0 && c.n + 1 < a.n_seqs) {
-        ++c.n;
-        cursor_load(a, c, kt);
+    if (++c.sub == subs) {
+        c.sub = 0;
+        if (++c.n >= a.n_seqs) return false;
+        cursor_load<C>(a, c);
     }
+    return true;
 }
 
 template <typename IO, int D, int R>
@@ -436,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             tc::mbar_init(&full[i], 1);
-            tc::mbar_init(&empty[i], kTeamWarps);
+            tc::mbar_init(&empty[i], C::TW);
         }
         tc::fence_mbar_init();
         s_dead = 0;
@@ -444,27 +480,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     tc::grid_dependency_sync();
     int bad = 0;
     const Place pl = find_place(
-        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, C::KT, &bad) * subs; }, blockIdx.x, gridDim.x, s_warp,
-        &s_place);
+        a.n_seqs, [&](int n) { return cost_of<C>(a, n, subs, &bad); }, blockIdx.x, gridDim.x, s_warp, &s_place);
     if (bad && blockIdx.x == 0) atomicMax(&g_decode_attn_error, bad);
-    const int64_t begin = pl.at;
-    const int64_t count = pl.n < 0 ? 0 : pl.total * (blockIdx.x + 1) / pl.blocks - begin;
     // contexts of no keys: zeros, a sequence's rows by one block
     for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
         const SeqRows r = seq_rows(a, n);
         if (!r.bad && r.n_kv == 0)
             for (int i = tid; i < a.HQ * D; i += kThreads) store_elem((IO*)a.o, (int64_t)n * a.HQ * D + i, 0.f);
     }
-    if (count <= 0) return;
+    const Partials part = partials(a.ws, R, D);
+    if (tid == 0) {      // for the join
+        int4 d = make_int4(-1, 0, 0, 0);
+        if (pl.n >= 0) {
+            const int tiles = tiles_of(a, pl.n, C::KT, &bad);
+            const int sub = (int)((pl.at - pl.before) / (tiles + C::kItemCost));
+            // unit of the item's first tile, and the blocks that hold its tiles: unit u is in the
+            // last block that begins at or before it
+            const int64_t t0 = pl.before + (int64_t)sub * (tiles + C::kItemCost) + C::kItemCost, N = pl.total;
+            const int c0 = (int)(((t0 + 1) * pl.blocks - 1) / N);
+            if (pl.at > t0 && (int)blockIdx.x == c0 + 1)
+                d = make_int4(c0, (int)(((t0 + tiles) * pl.blocks - 1) / N), pl.n, sub / hb * G + sub % hb * R);
+        }
+        part.desc[blockIdx.x] = d;
+    }
+    if (pl.n < 0) return;
 
+    const int64_t end = pl.total * (blockIdx.x + 1) / pl.blocks;
     Cursor cur;
     cur.n = pl.n;
-    cursor_load(a, cur, C::KT);
+    cursor_load<C>(a, cur);
     {
-        const int64_t in_seq = begin - pl.before;
-        cur.sub = (int)(in_seq / cur.tiles);
-        cur.tile = (int)(in_seq - (int64_t)cur.sub * cur.tiles);
+        const int64_t in_seq = pl.at - pl.before;
+        cur.sub = (int)(in_seq / (cur.tiles + C::kItemCost));
+        const int u = (int)(in_seq - (int64_t)cur.sub * (cur.tiles + C::kItemCost));
+        cur.tile = max(u - C::kItemCost, 0);
+        cur.unit = pl.at + max(C::kItemCost - u, 0);
     }
+    if (cur.unit >= end) return;       // the share ends within an item's cost: no tile
     const int rows_box = min(1 << a.kv.page_shift, C::KT);
 
     if (warp == kConsumers / 32) {
@@ -474,8 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
         const int64_t none = (int64_t)a.kv.n_pages << a.kv.page_shift;        // a row past the cache: zero fill
         int ent = 0, ent_n = -1, ent_base = 0;      // 32 table entries, one a lane
         bool ok = true;
-        for (int64_t it = 0; it < count; ++it) {
-            const int st = (int)(it % S);
+        bool more = true;
+        for (int it = 0; more; ++it) {
+            const int st = it % S;
             const uint32_t ph = (uint32_t)((it / S) & 1);
             if (it >= S && ok) {
                 ok = tc::mbar_wait(&empty[st], ph ^ 1);
@@ -508,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 tc::tma_load_3d(tile + (lk * C::NB + lb) * C::kBlk + lg * rows_box * 128, lk ? &tv : &tk, &full[st],
                                 lb * (128 / (int)sizeof(IO)), kvh, (int)row);
             }
-            cursor_next(a, cur, C::KT, subs, count - 1 - it);
+            more = cursor_next<C>(a, cur, subs, end);
         }
         if (!ok) {      // an expired wait: let every copy that was issued land before leaving
             if (lane == 0) atomicMax(&g_decode_attn_error, GDN_DEVERR_TIMEOUT);
@@ -518,12 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     }
 
     // ---- consumers
-    const int team = warp >> 2, w = warp & 3;
+    const int team = warp / C::TW, w = warp % C::TW;
     Warp<IO, D, R> st;
     const float sc = a.scale * kLog2e;
-    const Partials part = partials(a.ws, R, D);
-    bool ok = true, fresh = true, from_start = false;
-    for (int64_t it = 0; it < count; ++it) {
+    bool ok = true, fresh = true, from_start = false, more = true;
+    for (int it = 0; more; ++it) {
         const int kvh = cur.sub / hb, h0 = kvh * G + (cur.sub - kvh * hb) * R;
         const int rows = min(R, (kvh + 1) * G - h0);
         const int64_t qrow = ((int64_t)cur.n * a.HQ + h0) * D;
@@ -537,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             st.start((const IO*)a.q + qrow, rows, sq);
             fresh = false;
         }
-        if ((int)(it & 1) == team) {
-            const int s = (int)(it % S);
+        if (it % C::Teams == team) {
+            const int s = it % S;
             if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], (uint32_t)((it / S) & 1)));
             const int valid = min(C::KW, cur.len - cur.tile * C::KT - w * C::KW);
             if (ok && valid > 0) st.step(ring + s * C::kStage, w, valid, rows, sc, sq);
@@ -546,7 +598,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             if (lane == 0) tc::mbar_arrive(&empty[s]);
         }
         const bool item_end = cur.tile + 1 == cur.tiles;
-        if (item_end || it + 1 == count) {
+        more = cursor_next<C>(a, cur, subs, end);
+        if (item_end || !more) {
             // the segment is over: join the eight warps
             if (!ok && lane == 0) s_dead = 1;
             st.put(merge + warp * R * (D + 4), rows);
@@ -588,63 +641,56 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             tc::named_bar(1, kConsumers);
             fresh = true;
         }
-        cursor_next(a, cur, C::KT, subs, count - 1 - it);
     }
     if (s_dead && tid == 0) atomicMax(&g_decode_attn_error, GDN_DEVERR_TIMEOUT);
 }
 
-// Joins the pieces of the items that more than one block took.  Block (c, r): if block c of the
-// first kernel began inside an item, and is the first that did, row r of that item.
-constexpr int kJoinThreads = 256;
+// Joins the pieces of the items that more than one block took.  Block (c - 1, r): row r of the item
+// that block c of the first kernel left to it.  A warp takes every eighth piece, kBatch of them in
+// flight.
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kBatch = 8;
+template <int E> struct Vec;
+template <> struct Vec<2> { using T = float2; };
+template <> struct Vec<4> { using T = float4; };
 template <typename IO, int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int hb, int grid) {
-    constexpr int KT = Cfg<IO, D, R>::KT, E = D / 32;
-    __shared__ int64_t s_warp[kJoinThreads / 32];
-    __shared__ Place s_place;
-    __shared__ float s_o[8][D];
-    __shared__ float s_m[8], s_l[8];
-    const int c = blockIdx.x + 1, r = blockIdx.y, tid = threadIdx.x;
-    const int G = a.HQ / a.HKV, subs = a.HKV * hb;
-    int bad = 0;
-    // (before the wait: the first kernel only lets this one start once what ran before it is over,
-    // so the lengths are there, and the first kernel does not write them)
-    const Place pl = find_place(
-        a.n_seqs, [&](int n) { return (int64_t)tiles_of(a, n, KT, &bad) * subs; }, c, grid, s_warp, &s_place);
-    int first = -1, last = 0, kvh = 0, h0 = 0;
-    if (pl.n >= 0) {
-        const int tiles = tiles_of(a, pl.n, KT, &bad);
-        const int sub = (int)((pl.at - pl.before) / tiles);
-        const int64_t t0 = pl.before + (int64_t)sub * tiles, N = pl.total;
-        // blocks that hold tiles of the item [t0, t0 + tiles): the first is the last one that begins
-        // at or before t0
-        const int c0 = (int)(((t0 + 1) * pl.blocks - 1) / N);
-        kvh = sub / hb;
-        h0 = kvh * G + (sub - kvh * hb) * R;
-        if (pl.at != t0 && c == c0 + 1 && h0 + r < (kvh + 1) * G) {
-            first = c0;
-            last = (int)(((t0 + tiles) * pl.blocks - 1) / N);
-        }
-    }
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
+    constexpr int E = D / 32;
+    __shared__ float s_o[kJoinWarps][D];
+    __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     tc::grid_dependency_sync();
-    if (first < 0) return;
     const Partials part = partials(a.ws, R, D);
-    const int w = tid >> 5, lane = tid & 31;
+    const int4 d = part.desc[blockIdx.x + 1];
+    const int first = d.x, last = d.y, r = blockIdx.y, G = a.HQ / a.HKV;
+    if (first < 0 || d.w % G + r >= G) return;
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
     auto slot = [&](int b) { return ((int64_t)b * 2 + (b == first ? 1 : 0)) * R + r; };
-    // a warp every eighth piece, with its own running maximum
     float m = -INFINITY, l = 0.f, x[E] = {};
-#pragma unroll 2
-    for (int b = first + w; b <= last; b += 8) {
-        const float2 ml = part.ml[slot(b)];
-        const float* p = part.o + slot(b) * D + lane * E;
-        float y[E];
+    for (int b0 = first + w; b0 <= last; b0 += kBatch * kJoinWarps) {
+        float2 ml[kBatch];
+        typename Vec<E>::T y[kBatch];
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = p[e];
-        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-        const float f = exp2f(ml.x - base), g = exp2f(m - base);
+        for (int i = 0; i < kBatch; ++i) {
+            const int b = min(b0 + i * kJoinWarps, last);          // (past the end: read again, not used)
+            ml[i] = part.ml[slot(b)];
+            y[i] = reinterpret_cast<const typename Vec<E>::T*>(part.o + slot(b) * D)[lane];
+        }
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) mn = fmaxf(mn, ml[i].x);
+        const float base = mn == -INFINITY ? 0.f : mn, g = exp2f(m - base);
         m = mn;
-        l = fmaf(l, g, f * ml.y);
+        l *= g;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[e] = fmaf(x[e], g, f * y[e]);
+        for (int e = 0; e < E; ++e) x[e] *= g;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+            if (b0 + i * kJoinWarps <= last) {
+                const float f = exp2f(ml[i].x - base);
+                const float* v = reinterpret_cast<const float*>(&y[i]);
+                l = fmaf(f, ml[i].y, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = fmaf(f, v[e], x[e]);
+            }
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = x[e];
@@ -655,16 +701,18 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
     __syncthreads();
     if (tid < D) {
         m = s_m[0];
-        for (int i = 1; i < 8; ++i) m = fmaxf(m, s_m[i]);
+#pragma unroll
+        for (int i = 1; i < kJoinWarps; ++i) m = fmaxf(m, s_m[i]);
         const float base = m == -INFINITY ? 0.f : m;
         float y = 0.f, sum = 0.f;
-        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
             const float f = exp2f(s_m[i] - base);
             y = fmaf(f, s_o[i][tid], y);
             sum = fmaf(f, s_l[i], sum);
         }
         y /= sum;
-        const int64_t at = ((int64_t)pl.n * a.HQ + h0 + r) * D + tid;
+        const int64_t at = ((int64_t)d.z * a.HQ + d.w + r) * D + tid;
         store_elem((IO*)a.o, at, a.z ? gate_out(y, load_elem((const IO*)a.z, at)) : y);
     }
 }
@@ -688,8 +736,11 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     const int page = 1 << a.kv.page_shift;
     const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(IO)), 1, (cuuint32_t)(page < C::KT ? page : C::KT)};
     const CUtensorMapDataType dt = sizeof(IO) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
-    if (!make_map(&tk, dt, a.kv.k, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
-        !make_map(&tv, dt, a.kv.v, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+    // a head's row of 128 bytes has another head's beside it, which this block does not read next
+    const CUtensorMapL2promotion l2 =
+        D * sizeof(IO) == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B;
+    if (!make_map(&tk, dt, a.kv.k, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, l2) ||
+        !make_map(&tv, dt, a.kv.v, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, l2))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     e = allow_smem((const void*)attn_decode_kernel<IO, D, R>, C::kSmem, done);
@@ -699,7 +750,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     count_launch();
     if (grid == 1) return cudaSuccess;           // nothing to join
     e = launch_pdl(attn_join_kernel<IO, D, R>, dim3((unsigned)(grid - 1), (unsigned)(G < R ? G : R)), dim3(kJoinThreads), 0,
-                   s, a, hb, grid);
+                   s, a);
     if (e == cudaSuccess) count_launch();
     return e;
 }
@@ -717,7 +768,7 @@ cudaError_t launch_f32(const AttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 size_t attn_decode_bytes(int D) {
-    return kStatusBytes + (size_t)kMaxGrid * 2 * 16 * (sizeof(float2) + (size_t)D * 4);
+    return kStatusBytes + (size_t)kMaxGrid * (sizeof(int4) + 2 * 16 * (sizeof(float2) + (size_t)D * 4));
 }
 
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {

@@ -114,7 +114,8 @@ cudaError_t launch_decode_conv(bool bf16, const DecodeConv& conv, const DecodeGa
 // Tiled tensor map (element strides 1, no interleave, zero fill out of range); false if the
 // driver entry point is missing or the encoder rejects the arguments.
 bool make_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const cuuint64_t* dims,
-              const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw);
+              const cuuint64_t* strides, const cuuint32_t* box, CUtensorMapSwizzle sw,
+              CUtensorMapL2promotion l2 = CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 
 // Causal depthwise convolution of kernel 4 over whole sequences (dense when cu is null:
 // n_seqs sequences of T tokens): x [n_tokens, C] with C = 2 qk + (v channels), written to
