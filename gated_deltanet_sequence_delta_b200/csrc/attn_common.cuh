@@ -70,6 +70,8 @@ struct AttnPlan {
                                 // plan), or 0: whole tiles
     PlanTile* tiles;            // longest key range first
     int4* redo;                 // {sequence, key-value head, first row, rows} of that head's (token, query head) rows
+    int4* desc;                 // split plans, [block]: {tile, key-value head, first, last block} of the one the block began
+                                // inside, as the first that did; or tile = -1
     float2* part_ml;            // pieces of tiles that blocks share: [block][2][256] (maximum, sum), and
     float* part_o;              // [block][2][256][D]
     int max_tiles, max_redo;

@@ -177,6 +177,8 @@ AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per
     at += up((size_t)tiles * redo * sizeof(int4));
     // with more tiles than this, whole ones keep the blocks evenly busy
     p.can_split = split_heads > 0 && tiles * split_heads <= 4 * kSplitGrid && tiles <= kSplitTiles;
+    p.desc = reinterpret_cast<int4*>(b + at);
+    if (p.can_split) at += up(kSplitGrid * sizeof(int4));
     p.part_ml = reinterpret_cast<float2*>(b + at);
     if (p.can_split) at += (size_t)kSplitGrid * 2 * kSplitRows * sizeof(float2);
     p.part_o = reinterpret_cast<float*>(b + at);

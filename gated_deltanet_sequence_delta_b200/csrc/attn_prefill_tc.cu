@@ -15,22 +15,25 @@
 // runs, the tensor cores work for the other.  Blocks are persistent, so that an item's first
 // loads and scores run under the last item's outputs.
 //
-// Roles (12 warps, one block per SM; the last only completes a warpgroup):
+// Roles (12 warps, one block per SM):
 //   warps 0-3, 4-7   softmax of tile A, of tile B: a thread owns a row (TMEM lane), takes its 128
 //                    scores into registers, forms the weights, writes them as bf16
 //   warps 8, 9       issue the MMAs of tile A, of tile B: per step  S = Q K',  O += P V  (K' the
 //                    next step's keys); two warps, so that neither tile's products wait behind
 //                    the other's softmax
-//   warp 10          TMA: queries once, then keys and values through a ring
+//   warps 10, 11     TMA: the work items, their queries and the keys; the values.  Keys and values
+//                    go through one ring
 // TMEM, 512 columns: S 128, P_A and P_B 64 each, O_A and O_B D each.  A tile's scores of the next
 // step are formed while its softmax works on the last ones, so that the products stay off that
 // chain; at D = 128 this leaves room for one S, which the tiles use in turn (it is free again
 // once its softmax warps have read it), at D = 64 for one each.
 //
-// The reference m moves only when a row's maximum has grown by more than 2^8 since it was set:
-// weights then stay below 2^8, sums and products in fp32 lose nothing, and the accumulated O has
-// to be rescaled in tensor memory only in a row's first steps.  The weights are rounded to bf16
-// for the product (half a step, 2^-8 relative, each); their sum is taken before the rounding.
+// The reference m need not be the running maximum, only near it: weights up to 2^15 lose nothing in
+// fp32 sums and products, nor in bf16's range.  So a step first forms its weights against m as it
+// is, without looking for a maximum, and keeps them unless a row's sum exceeds 2^15; only then (and
+// where a mask cuts the step) are the maxima found, m moved where it has been passed by more than
+// 2^8, and the accumulated O rescaled in tensor memory: a row's first steps.  The weights are rounded
+// to bf16 for the product (half a step, 2^-8 relative, each); their sum is taken before the rounding.
 //
 // Masked weights are exact zeros, but 0 * v is not 0 where v is infinite or NaN.  Values past
 // the last key that any row of the block sees are cleared in shared memory; a value inside the
@@ -51,9 +54,10 @@ constexpr int kThreads = 384;
 // keeps 72 (2 x 216 + 72 = 3 x 168).
 constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr int kRows = 128, kKeys = 128;
-constexpr int kItems = 4;                // work items known ahead
+constexpr int kItems = 8;                // work items known ahead
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 8.0f;            // growth of the maximum (log2) that moves the reference
+constexpr float kGrow = 8.0f;            // growth of the maximum (log2) that moves the reference,
+constexpr float kGrowSum = 32768.0f;     // where it is looked at: when a step's weights sum to more than this
 
 template <int D>
 struct Cfg {
@@ -187,6 +191,72 @@ __device__ __forceinline__ void list_redo(const AttnPlan& plan, int n, int kvh, 
     if (k < plan.max_redo) plan.redo[k] = make_int4(n, kvh, row, rows);
 }
 
+// The items of this block, in order.  Warp-wide.
+struct ItemSource {
+    int tiles, shared, k;
+    int64_t at, stop;
+    __device__ __forceinline__ ItemSource(const AttnArgs& a, const AttnPlan& plan, int tokens) {
+        tiles = plan.counts[0];
+        shared = plan.counts[3];
+        k = 0;
+        at = stop = 0;
+        if (shared == 0 || (int)blockIdx.x >= shared) return;
+        // an even share of all steps, tile by tile, key-value head by key-value head
+        const int lane = threadIdx.x & 31;
+        const PlanTile end = plan.tiles[tiles - 1];
+        const int64_t N = (int64_t)(end.before + end.steps) * a.HKV;
+        at = N * blockIdx.x / shared;
+        stop = N * (blockIdx.x + 1) / shared;
+        for (int b = 0; b < tiles; b += 32) {          // the tile that holds step `at`
+            const bool in = b + lane < tiles && (int64_t)plan.tiles[b + lane].before * a.HKV <= at;
+            const unsigned m = __ballot_sync(0xffffffffu, in);
+            if (m) k = b + 31 - __clz(m);
+        }
+        if (lane == 0 && blockIdx.x > 0) {             // for the join
+            const PlanTile t = plan.tiles[k];
+            const int h = (int)((at - (int64_t)t.before * a.HKV) / t.steps);
+            // the (tile, head)'s blocks: the first is the last one that begins at or before its
+            // first step (no block is empty: there are at least as many steps as blocks)
+            const int64_t t0 = (int64_t)t.before * a.HKV + (int64_t)h * t.steps;
+            const int c0 = (int)(((t0 + 1) * shared - 1) / N), c1 = (int)(((t0 + t.steps) * shared - 1) / N);
+            plan.desc[blockIdx.x] =
+                at > t0 && (int)blockIdx.x == c0 + 1 ? make_int4(k, h, c0, c1) : make_int4(-1, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void next(const AttnArgs& a, const AttnPlan& plan, int tokens, Item& it) {
+        const int G = a.HQ / a.HKV, lane = threadIdx.x & 31;
+        while (true) {
+            if (shared == 0) {
+                // whole tiles: the list runs from long to short; blocks take it forwards and
+                // backwards in turn, which evens out their sums
+                const int64_t i = (int64_t)k * gridDim.x + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+                if (i >= (int64_t)tiles * a.HKV) break;
+                ++k;
+                const PlanTile t = plan.tiles[i / a.HKV];
+                it = Item{t.n, (int)(i % a.HKV), t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, 0, t.steps, -1};
+            } else {
+                if (at >= stop) break;
+                const PlanTile t = plan.tiles[k];
+                const int64_t o = at - (int64_t)t.before * a.HKV;
+                const int h = (int)(o / t.steps);
+                if (h >= a.HKV) {
+                    ++k;
+                    continue;
+                }
+                const int s0 = (int)(o - (int64_t)h * t.steps), s1 = (int)min((int64_t)t.steps, s0 + stop - at);
+                it = Item{t.n, h, t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, s0, s1,
+                          s0 == 0 && s1 == t.steps ? -1 : (int)blockIdx.x * 2 + (s0 == 0 ? 1 : 0)};
+                at += s1 - s0;
+            }
+            if (it.total(tokens) > 0) return;
+            // no row of the tile sees a key: the CUDA-core kernel writes its zeros
+            for (int row = lane * 64; row < 2 * tokens * G; row += 32 * 64)
+                list_redo(plan, it.n, it.kvh, it.tok * G + row, min(64, 2 * tokens * G - row));
+        }
+        it.slot = -2;
+    }
+};
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_constant__ CUtensorMap tq,
                                                                    const __grid_constant__ CUtensorMap tk,
@@ -253,63 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        if (warp == 10) {
-            // ---- loads ------------------------------------------------------------------
-            bool ok = true;
-            const int boxes = kKeys / box_rows;
-            const int lg = lane / C::kHalves, lh = lane % C::kHalves;  // this lane's box, its column block
-            const int none = (int)((int64_t)a.kv.n_pages << a.kv.page_shift);
-            int t = 0, items = 0;
-            for (int r = 0; ok; ++r) {
-                const Item it = item_at(r, ok);
-                item_done(r);
-                if (it.slot == -2) break;
-                const int total = it.total(tokens);
-                for (int u = 0; u < 2 * total; ++u, ++t) {             // K_0, (Q), K_1, V_0, K_2, V_1, ..., V_last
-                    const bool is_v = u + 1 == 2 * total || (u > 0 && (u & 1) == 0);
-                    const int step = u + 1 == 2 * total ? total - 1 : is_v ? (u >> 1) - 1 : (u + 1) >> 1;
-                    if (u == 1) {
-                        if (items > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty, (uint32_t)(items - 1) & 1u));
-                        if (!ok) break;
-                        if (lane == 0) {
-                            const int tiles = it.ntok(1, tokens) > 0 ? 2 : 1;
-                            tc::mbar_expect_tx(&q_full, (uint32_t)(tiles * C::kHalves * tokens * G * 128));
-                            for (int x = 0; x < tiles; ++x)
-                                for (int h = 0; h < C::kHalves; ++h)
-                                    tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tq, &q_full, h * 64, it.kvh * G,
-                                                    it.q0 + it.tok + x * tokens);
-                        }
-                        __syncwarp();
-                        ++items;
-                    }
-                    const int s = t % S;
-                    const int pos = (it.s0 + step) * kKeys + lg * box_rows;
-                    int row = it.q0 + pos;
-                    if (a.kv.table && lg < boxes) {
-                        row = none;                                    // past the cache: zero fill
-                        if (pos < it.n_kv) {
-                            const int64_t c = cache_row(a.kv.table + (int64_t)it.n * a.kv.max_pages, pos, a.kv.page_shift,
-                                                        a.kv.n_pages);
-                            if (c >= 0)
-                                row = (int)c;
-                            else
-                                atomicMax(&g_attn_tc_error, GDN_DEVERR_PAGE);
-                        }
-                    }
-                    if (t >= S) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[s], (uint32_t)((t / S) & 1) ^ 1u));
-                    if (!ok) break;
-                    if (lane == 0) tc::mbar_expect_tx(&kv_full[s], C::kTile);
-                    __syncwarp();
-                    if (lg < boxes)
-                        tc::tma_load_3d(ring + s * C::kTile + lh * C::kHalf + lg * box_rows * 128, is_v ? &tv : &tk,
-                                        &kv_full[s], lh * 64, it.kvh, row);
-                }
-            }
-            if (!ok) {       // an expired wait: give the copies under way time to land
-                if (lane == 0) s_timeout = 1;
-                for (int i = 0; i < S; ++i) tc::mbar_wait(&kv_full[i], (uint32_t)(((t - 1 - i) / S) & 1), 1000000);
-            }
-        } else if (warp < 10) {
+        if (warp < 10) {
             // ---- products of tile x ---------------------------------------------------------
             // (the whole warp walks the loop, one elected lane issues)
             const int x = warp - 8;
@@ -387,65 +401,102 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             __syncwarp();
             if (!tc::mbar_wait(&drain[x], 0) || !ok) s_timeout = 1;
         } else {
-            // ---- items: read ahead of the roles, so that no one waits for the list -------------------
-            const int tiles = plan.counts[0], shared = plan.counts[3];
+            // ---- loads: warp 10 the items, queries and keys, warp 11 the values ------------------
+            // The ring takes K(0), K(1), V(0), K(2), V(1), ..., V(last) of an item.  (Its slots pass
+            // between the two warps; what was in one two turns ago is long used by then, since the
+            // products use the tiles in order.)
+            const bool is_v = warp == 11;
+            const CUtensorMap* map = is_v ? &tv : &tk;
+            const int boxes = kKeys / box_rows;
+            const int lg = lane / C::kHalves, lh = lane % C::kHalves;  // this lane's box, its column block
+            const int none = (int)((int64_t)a.kv.n_pages << a.kv.page_shift);
+            const bool paged = a.kv.table != nullptr && lg < boxes;
             bool ok = true;
-            int r = 0;
-            auto put = [&](const Item& it) {
-                if (it.slot != -2 && it.total(tokens) == 0) {
-                    // no row of the tile sees a key: the CUDA-core kernel writes its zeros
-                    for (int row = lane * 64; row < 2 * tokens * G; row += 32 * 64)
-                        list_redo(plan, it.n, it.kvh, it.tok * G + row, min(64, 2 * tokens * G - row));
-                    return;
-                }
-                if (r >= kItems) ok = __all_sync(0xffffffffu, tc::mbar_wait(&item_empty[r % kItems], (uint32_t)(r / kItems - 1) & 1u));
-                if (ok && lane == 0) {
-                    s_item[r % kItems] = it;
-                    tc::mbar_arrive(&item_full[r % kItems]);
-                }
-                __syncwarp();
-                ++r;
+            int t0 = 0;                                                // ring tiles before this item
+            // This lane's page of a step, read ahead: a copy must not wait for its address.
+            auto entry = [&](const Item& it, int step) {
+                const int pos = (it.s0 + step) * kKeys + lg * box_rows;
+                return paged && pos < it.n_kv ? a.kv.table[(int64_t)it.n * a.kv.max_pages + (pos >> a.kv.page_shift)] : 0;
             };
-            Item it = {};
-            if (shared == 0) {
-                // whole tiles: the list runs from long to short; blocks take it forwards and
-                // backwards in turn, which evens out their sums
-                const int64_t count = (int64_t)tiles * a.HKV;
-                for (int j = 0; ok; ++j) {
-                    const int64_t i = (int64_t)j * gridDim.x + ((j & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-                    if (i >= count) break;
-                    const PlanTile t = plan.tiles[i / a.HKV];
-                    put(Item{t.n, (int)(i % a.HKV), t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, 0, t.steps, -1});
-                }
-            } else if ((int)blockIdx.x < shared) {
-                // an even share of all steps, tile by tile, key-value head by key-value head
-                const PlanTile end = plan.tiles[tiles - 1];
-                const int64_t N = (int64_t)(end.before + end.steps) * a.HKV;
-                int64_t at = N * blockIdx.x / shared;
-                const int64_t stop = N * (blockIdx.x + 1) / shared;
-                int k = 0;                                         // the tile that holds step `at`
-                for (int b = 0; b < tiles; b += 32) {
-                    const bool in = b + lane < tiles && (int64_t)plan.tiles[b + lane].before * a.HKV <= at;
-                    const unsigned m = __ballot_sync(0xffffffffu, in);
-                    if (m) k = b + 31 - __clz(m);
-                }
-                for (; ok && at < stop; ++k) {
-                    const PlanTile t = plan.tiles[k];
-                    int64_t o = at - (int64_t)t.before * a.HKV;
-                    for (int h = (int)(o / t.steps); ok && h < a.HKV && at < stop; ++h) {
-                        const int s0 = (int)(o - (int64_t)h * t.steps);
-                        const int s1 = (int)min((int64_t)t.steps, s0 + stop - at);
-                        const bool whole = s0 == 0 && s1 == t.steps;
-                        put(Item{t.n, h, t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, s0, s1,
-                                    whole ? -1 : (int)blockIdx.x * 2 + (s0 == 0 ? 1 : 0)});
-                        at += s1 - s0;
-                        o += s1 - s0;
+            auto load = [&](const Item& it, int step, int t, int page) {
+                const int pos = (it.s0 + step) * kKeys + lg * box_rows, slot = t % S;
+                int row = it.q0 + pos;
+                if (paged) {
+                    row = none;                                        // past the context or the cache: zero fill
+                    if (pos < it.n_kv) {
+                        if (page >= 0 && page < a.kv.n_pages)
+                            row = (page << a.kv.page_shift) + (pos & ((1 << a.kv.page_shift) - 1));
+                        else
+                            atomicMax(&g_attn_tc_error, GDN_DEVERR_PAGE);
                     }
                 }
+                if (t >= S) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[slot], (uint32_t)((t / S) & 1) ^ 1u));
+                if (!ok) return;
+                if (lane == 0) tc::mbar_expect_tx(&kv_full[slot], C::kTile);
+                __syncwarp();
+                if (lg < boxes)
+                    tc::tma_load_3d(ring + slot * C::kTile + lh * C::kHalf + lg * box_rows * 128, map, &kv_full[slot], lh * 64,
+                                    it.kvh, row);
+            };
+            if (is_v) {
+                for (int r = 0; ok; ++r) {
+                    const Item it = item_at(r, ok);
+                    item_done(r);
+                    if (it.slot == -2) break;
+                    const int total = it.total(tokens);
+                    int page = entry(it, 0);
+                    for (int j = 0; j < total && ok; ++j) {
+                        const int after = entry(it, j + 1);
+                        load(it, j, t0 + (j + 1 < total ? 2 * j + 2 : 2 * j + 1), page);
+                        page = after;
+                    }
+                    t0 += 2 * total;
+                }
+            } else {
+                ItemSource src(a, plan, tokens);
+                Item it, ahead;
+                int r = 0;
+                auto put = [&](const Item& x) {                        // to the other roles
+                    if (r >= kItems) ok = __all_sync(0xffffffffu, tc::mbar_wait(&item_empty[r % kItems], (uint32_t)(r / kItems - 1) & 1u));
+                    if (ok && lane == 0) {
+                        s_item[r % kItems] = x;
+                        tc::mbar_arrive(&item_full[r % kItems]);
+                    }
+                    __syncwarp();
+                    ++r;
+                };
+                src.next(a, plan, tokens, it);
+                put(it);
+                while (ok && it.slot != -2) {
+                    const int total = it.total(tokens);
+                    int page = entry(it, 0);
+                    for (int j = 0; j < total && ok; ++j) {
+                        const int after = entry(it, j + 1);
+                        load(it, j, t0 + (j == 0 ? 0 : 2 * j - 1), page);
+                        page = after;
+                        if (j > 0 || !ok) continue;
+                        // with the first keys, the queries, and the next item for everyone
+                        if (r > 1) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty, (uint32_t)(r - 2) & 1u));
+                        if (ok && tc::elect_one()) {
+                            const int tiles = it.ntok(1, tokens) > 0 ? 2 : 1;
+                            tc::mbar_expect_tx(&q_full, (uint32_t)(tiles * C::kHalves * tokens * G * 128));
+                            for (int x = 0; x < tiles; ++x)
+                                for (int h = 0; h < C::kHalves; ++h)
+                                    tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tq, &q_full, h * 64, it.kvh * G,
+                                                    it.q0 + it.tok + x * tokens);
+                        }
+                        __syncwarp();
+                        src.next(a, plan, tokens, ahead);
+                        put(ahead);
+                    }
+                    t0 += 2 * total;
+                    it = ahead;
+                }
             }
-            it.slot = -2;
-            if (ok) put(it);
-            if (!ok && lane == 0) s_timeout = 1;
+            if (!ok) {       // an expired wait: give the copies under way time to land
+                if (lane == 0) s_timeout = 1;
+                for (int i = 0; i < S; ++i) tc::mbar_wait(&kv_full[i], 0, 1000000);
+            }
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
@@ -495,73 +546,79 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 }
                 if (lane == 0 && next >= 0) tc::mbar_arrive(&turn[next]);
                 const int j0 = i * kKeys;
-                const bool masked = __any_sync(0xffffffffu, j0 + kKeys - 1 > lim);
-                if (masked) {
-#pragma unroll
-                    for (int j = 0; j < 128; ++j)
-                        if (j0 + j > lim) s[j] = -INFINITY;
-                }
-                float mx = max3(s[0], s[1], s[2]), mx1 = max3(s[3], s[4], s[5]), mx2 = max3(s[6], s[7], s[8]),
-                      mx3 = max3(s[9], s[10], s[11]);
-#pragma unroll
-                for (int j = 12; j < 124; j += 8) {
-                    mx = max3(mx, s[j], s[j + 1]);
-                    mx1 = max3(mx1, s[j + 2], s[j + 3]);
-                    mx2 = max3(mx2, s[j + 4], s[j + 5]);
-                    mx3 = max3(mx3, s[j + 6], s[j + 7]);
-                }
-                mx = max3(mx, s[124], s[125]);
-                mx1 = max3(mx1, s[126], s[127]);
-                mx = max3(mx, mx1, fmaxf(mx2, mx3)) * sc;
-                if (!(mx == mx)) mx = INFINITY;         // (-inf * 0: nothing seen, or scale 0 and infinite scores)
-                const bool none = lim < j0;              // no key of this step is seen: m and l stay
-                if (none) mx = -INFINITY;
-                const bool move = mx > m + kGrow || (m == -INFINITY && !none);
-                if (move && mx == -INFINITY) finite = false;      // every key seen so far scores -inf
-                if (__any_sync(0xffffffffu, move)) {
-                    const float alpha = move && m != -INFINITY ? exp2_sfu(m - mx) : 1.f;
-                    if (move) {
-                        l *= alpha;
-                        m = mx;
-                    }
-                    if (i > 0) {
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
-                        if (!ok) break;
-                        tc::tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 16) {
-                            float o[16];
-                            tc::tmem_ld16(to + c, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= alpha;
-                            tc::tmem_st16_raw(to + c, reinterpret_cast<uint32_t*>(o));
-                        }
-                    }
-                }
-                if (clear_from - j0 < kKeys) {
-                    // values that no row of the block sees may be anything: clear them
-                    // (the MMA warp, which sees every copy land in turn, tells when they are there)
-                    const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&v_last[x], (uint32_t)lasts & 1u));
-                    if (!ok) break;
-                    uint8_t* v = ring + slot * C::kTile;
-                    const int first = clear_from - j0;
-                    for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
-                        const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
-                        *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                    }
-                    tc::fence_async_smem();
-                }
-                const float base = m == -INFINITY ? 0.f : m;
+                // Later steps that every row sees whole: the weights against the reference as it is.
+                // They stand if no row's sum says that it should have moved.
+                const bool masked = __any_sync(0xffffffffu, j0 + kKeys - 1 > lim || (m == -INFINITY && lim != INT32_MAX));
                 auto free = [&] {                        // the last step's product has read P
                     if (i > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
                     tc::tc_fence_after();
                 };
-                if (masked)
-                    l += weights<true, C::kPoly>(s, sc, base, lim - j0, tp, free);
-                else
-                    l += weights<false, C::kPoly>(s, sc, base, 0, tp, free);
+                bool stand = false;
+                if (!masked) {
+                    const float sum = weights<false, C::kPoly>(s, sc, m, 0, tp, free);
+                    stand = !__any_sync(0xffffffffu, !(sum <= kGrowSum) && lim != INT32_MAX);
+                    if (stand) l += sum;
+                }
+                if (!ok) break;
+                if (!stand) {
+#pragma unroll
+                    for (int j = 0; j < 128; ++j)
+                        if (j0 + j > lim) s[j] = -INFINITY;
+                    float mx = max3(s[0], s[1], s[2]), mx1 = max3(s[3], s[4], s[5]), mx2 = max3(s[6], s[7], s[8]),
+                          mx3 = max3(s[9], s[10], s[11]);
+#pragma unroll
+                    for (int j = 12; j < 124; j += 8) {
+                        mx = max3(mx, s[j], s[j + 1]);
+                        mx1 = max3(mx1, s[j + 2], s[j + 3]);
+                        mx2 = max3(mx2, s[j + 4], s[j + 5]);
+                        mx3 = max3(mx3, s[j + 6], s[j + 7]);
+                    }
+                    mx = max3(mx, s[124], s[125]);
+                    mx1 = max3(mx1, s[126], s[127]);
+                    mx = max3(mx, mx1, fmaxf(mx2, mx3)) * sc;
+                    if (!(mx == mx)) mx = INFINITY;         // (-inf * 0: nothing seen, or scale 0 and infinite scores)
+                    const bool none = lim < j0;              // no key of this step is seen: m and l stay
+                    if (none) mx = -INFINITY;
+                    const bool move = mx > m + kGrow || (m == -INFINITY && !none);
+                    if (move && mx == -INFINITY) finite = false;      // every key seen so far scores -inf
+                    if (__any_sync(0xffffffffu, move)) {
+                        const float alpha = move && m != -INFINITY ? exp2_sfu(m - mx) : 1.f;
+                        if (move) {
+                            l *= alpha;
+                            m = mx;
+                        }
+                        if (i > 0) {
+                            ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
+                            if (!ok) break;
+                            tc::tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                float o[16];
+                                tc::tmem_ld16(to + c, o);
+                                tc::tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] *= alpha;
+                                tc::tmem_st16_raw(to + c, reinterpret_cast<uint32_t*>(o));
+                            }
+                        }
+                    }
+                    if (clear_from - j0 < kKeys) {
+                        // values that no row of the block sees may be anything: clear them
+                        // (the MMA warp, which sees every copy land in turn, tells when they are there)
+                        const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&v_last[x], (uint32_t)lasts & 1u));
+                        if (!ok) break;
+                        uint8_t* v = ring + slot * C::kTile;
+                        const int first = clear_from - j0;
+                        for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
+                            const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
+                            *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_async_smem();
+                    }
+                    const float base = m == -INFINITY ? 0.f : m;
+                    l += weights<true, false>(s, sc, base, lim - j0, tp, free);
+                }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
                 __syncwarp();
@@ -658,69 +715,75 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     if (tid == 0 && s_timeout) atomicMax(&g_attn_tc_error, GDN_DEVERR_TIMEOUT);
 }
 
-// Joins the pieces of a split plan.  Block (c, y): if block c of the main kernel began inside a
-// tile's steps, and is the first that did, rows 32 y .. 32 y + 31 of that tile.
-constexpr int kJoinThreads = 256;
+// Joins the pieces of a split plan.  Block (c - 1, y): rows 16 y .. 16 y + 15 of the (tile, head) that
+// block c of the main kernel left to it, two rows a warp, kBatch pieces' loads in flight.
+constexpr int kJoinThreads = 256, kBatch = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a, AttnPlan plan, int tokens) {
     constexpr int E = D / 32;
     tc::grid_dependency_sync();
-    const int shared = plan.counts[3], tiles = plan.counts[0], c = blockIdx.x + 1;
-    if (c >= shared || tiles == 0) return;
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
-    const PlanTile end = plan.tiles[tiles - 1];
-    const int64_t N = (int64_t)(end.before + end.steps) * a.HKV;
-    auto start = [&](int b) { return N * b / shared; };
-    const int64_t at = start(c);
-    int k = 0;
-    for (int b = 0; b < tiles; b += 32) {
-        const bool in = b + lane < tiles && (int64_t)plan.tiles[b + lane].before * a.HKV <= at;
-        const unsigned m = __ballot_sync(0xffffffffu, in);
-        if (m) k = b + 31 - __clz(m);
-    }
-    const PlanTile t = plan.tiles[k];
-    const int h = (int)((at - (int64_t)t.before * a.HKV) / t.steps);
-    const int64_t t0 = (int64_t)t.before * a.HKV + (int64_t)h * t.steps, t1 = t0 + t.steps;
-    // the tile's blocks: the first is the last one that begins at or before t0 (no block is empty:
-    // there are at least as many steps as blocks)
-    const int c0 = (int)(((t0 + 1) * shared - 1) / N), c1 = (int)((t1 * shared - 1) / N);
-    if (at == t0 || c != c0 + 1) return;
-    const int G = a.HQ / a.HKV;
+    const int c = blockIdx.x + 1;
+    if (c >= plan.counts[3]) return;
+    const int4 d = plan.desc[c];
+    if (d.x < 0) return;
+    const PlanTile t = plan.tiles[d.x];
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, G = a.HQ / a.HKV, h = d.y;
+    const int r0 = blockIdx.y * 16, x = r0 / kRows;
+    const int tok0 = (t.index * 2 + x) * tokens;            // the half's first token
+    if (tok0 + (r0 - x * kRows) / G >= t.n_q) return;       // no row here
     bool finite = true;
-    const int r0 = blockIdx.y * 32;
-    for (int r = r0 + w; r < r0 + 32; r += kJoinThreads / 32) {
-        const int x = r / kRows, tr = r - x * kRows, tok = t.index * 2 * tokens + x * tokens + tr / G;
-        if (tr >= tokens * G || tok >= t.n_q) continue;
-        const int lim = t.n_kv - t.n_q + tok;
-        float m = -INFINITY, l = 0.f, o[E] = {};
-        auto piece = [&](int b) { return ((int64_t)b * 2 + (b == c0 ? 1 : 0)) * kSplitRows + r; };
-        for (int b = c0; b <= c1; ++b) m = fmaxf(m, plan.part_ml[piece(b)].x);
-        const float base = m == -INFINITY ? 0.f : m;
-        for (int b = c0; b <= c1; ++b) {
-            const float2 ml = plan.part_ml[piece(b)];
-            // a piece in which the row sees no key has no sums
-            const int s0 = b == c0 ? 0 : (int)(start(b) - t0);
-            if (lim < s0 * kKeys) continue;
-            float f;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"(ml.x - base));
-            l = fmaf(f, ml.y, l);
-            const float* p = plan.part_o + piece(b) * D + lane * E;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e], o[e]);
+    for (int i = 0; i < 2; ++i) {
+        const int r = r0 + 2 * w + i, tr = r - x * kRows, tok = tok0 + tr / G;
+        if (tr >= tokens * G || tok >= t.n_q) continue;
+        float m = -INFINITY, l = 0.f, o[E] = {};
+        for (int b0 = d.z; b0 <= d.w; b0 += kBatch) {
+            float2 ml[kBatch];
+            float y[kBatch][E];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const int b = min(b0 + k, d.w);                // (past the end: read again, not used)
+                const int64_t at = ((int64_t)b * 2 + (b == d.z ? 1 : 0)) * kSplitRows + r;
+                ml[k] = plan.part_ml[at];
+                const float* p = plan.part_o + at * D + lane * E;
+                if constexpr (E == 4)
+                    *reinterpret_cast<float4*>(y[k]) = *reinterpret_cast<const float4*>(p);
+                else
+                    *reinterpret_cast<float2*>(y[k]) = *reinterpret_cast<const float2*>(p);
+            }
+            float mn = m;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) mn = fmaxf(mn, ml[k].x);
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float g = exp2_sfu(m - base);
+            m = mn;
+            l *= g;
+#pragma unroll
+            for (int e = 0; e < E; ++e) o[e] *= g;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                // (a piece in which the row sees no key has no sums, whatever lies there)
+                if (b0 + k > d.w || (ml[k].x == -INFINITY && ml[k].y == 0.f)) continue;
+                const float f = exp2_sfu(ml[k].x - base);
+                l = fmaf(f, ml[k].y, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = fmaf(f, y[k][e], o[e]);
+            }
         }
+        const bool empty = t.n_kv - t.n_q + tok < 0;
         const int64_t to = (((int64_t)t.q0 + tok) * a.HQ + h * G + tr % G) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            float y = lim < 0 ? 0.f : o[e] / l;
-            finite = finite && fabsf(y) <= 3.4028235e38f;
-            if (a.z && lim >= 0) y = gate_out_fast(y, __bfloat162float(((const bf16*)a.z)[to + e]));
-            ((bf16*)a.o)[to + e] = __float2bfloat16_rn(y);
+            float v = empty ? 0.f : o[e] / l;
+            finite = finite && fabsf(v) <= 3.4028235e38f;
+            if (a.z && !empty) v = gate_out_fast(v, __bfloat162float(((const bf16*)a.z)[to + e]));
+            ((bf16*)a.o)[to + e] = __float2bfloat16_rn(v);
         }
     }
-    // (rows of the tile are listed as the (token, head) rows of the sequence)
+    // (rows are listed as the (token, head) rows of the sequence)
     if (__syncthreads_or(!finite) && tid == 0) {
-        const int x = r0 / kRows, tr = r0 - x * kRows;
-        list_redo(plan, t.n, h, (t.index * 2 + x) * tokens * G + tr, min(32, tokens * G - tr));
+        const int tr = r0 - x * kRows;
+        list_redo(plan, t.n, h, tok0 * G + tr, min(16, tokens * G - tr));
     }
 }
 
@@ -728,7 +791,7 @@ template <int D>
 cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     using C = Cfg<D>;
     const int G = a.HQ / a.HKV, tokens = kRows / G;
-    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 8 * a.HKV, 1, 2 * tokens, a.HKV, D);
+    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 16 * a.HKV, 1, 2 * tokens, a.HKV, D);
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -764,7 +827,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     count_launch();
     if (plan.can_split && grid > 1) {
-        e = launch_pdl(attn_join_rows_kernel<D>, dim3((unsigned)(grid - 1), kSplitRows / 32), dim3(kJoinThreads), 0, s, a,
+        e = launch_pdl(attn_join_rows_kernel<D>, dim3((unsigned)(grid - 1), kSplitRows / 16), dim3(kJoinThreads), 0, s, a,
                        plan, tokens);
         if (e != cudaSuccess) return e;
         count_launch();
@@ -777,7 +840,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 bool attn_tc_supported(int HQ, int HKV) { return HQ / HKV <= kRows; }
 
 size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D) {
-    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, 8 * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
+    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, 16 * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
     return p.bytes;
 }
 
