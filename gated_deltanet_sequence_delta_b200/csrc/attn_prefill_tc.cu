@@ -260,12 +260,14 @@ struct ItemSource {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_constant__ CUtensorMap tq,
                                                                    const __grid_constant__ CUtensorMap tk,
-                                                                   const __grid_constant__ CUtensorMap tv, AttnArgs a,
+                                                                   const __grid_constant__ CUtensorMap tv,
+                                                                   const __grid_constant__ CUtensorMap tz,
+                                                                   const __grid_constant__ CUtensorMap to_map, AttnArgs a,
                                                                    AttnPlan plan, int tokens, int box_rows) {
     using C = Cfg<D>;
     constexpr int S = C::kRing;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t q_full, q_empty, kv_full[S], kv_empty[S], s_full[2], turn[2], p_full[2], pv_done[2],
+    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], q_used[2], z_full[2], staged[2], kv_full[S], kv_empty[S], s_full[2], turn[2], p_full[2], pv_done[2],
         v_last[2], drain[2], item_full[kItems], item_empty[kItems];
     __shared__ Item s_item[kItems];
     __shared__ uint32_t s_tmem;
@@ -276,13 +278,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     const int G = a.HQ / a.HKV;
 
     if (tid == 0) {
-        tc::mbar_init(&q_full, 1);
-        tc::mbar_init(&q_empty, 2);
         for (int i = 0; i < S; ++i) {
             tc::mbar_init(&kv_full[i], 1);
             tc::mbar_init(&kv_empty[i], 2);
         }
         for (int x = 0; x < 2; ++x) {
+            tc::mbar_init(&q_full[x], 1);
+            tc::mbar_init(&q_empty[x], 1);
+            tc::mbar_init(&q_used[x], 1);
+            tc::mbar_init(&z_full[x], 1);
+            tc::mbar_init(&staged[x], 4);
             tc::mbar_init(&s_full[x], 1);
             tc::mbar_init(&turn[x], 4);
             tc::mbar_init(&p_full[x], 4);
@@ -332,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const uint64_t qd = tc::desc_sw128(tc::smem_u32(q_smem + x * C::kTile), 0, 1024);
             const uint64_t kd = tc::desc_sw128(tc::smem_u32(ring), 0, 1024), vd = tc::desc_sw128(tc::smem_u32(ring), C::kHalf, 1024);
             bool ok = true;
-            int t0 = 0, items = 0, mine = 0;                           // ring tiles, items and steps before this item
+            int t0 = 0, items = 0, loads = 0, mine = 0;                // ring tiles, items, queries and steps before this item
             int turns = -1;                                            // phases of turn[x] taken
             auto wait = [&](uint64_t* bar, int phase) {
                 if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, (uint32_t)phase & 1u));
@@ -344,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (it.slot == -2) break;
                 const int steps = it.steps(x, tokens), total = it.total(tokens);
                 if (items == 0 && C::kOneS && it.first(tokens) != x) turns = 0;
-                wait(&q_full, items);
+                if (steps > 0) wait(&q_full[x], loads++);
                 ++items;
                 for (int i = -1; i < total && ok; ++i) {               // S(i + 1), then O += P(i) V(i)
                     if (i + 1 < total) {
@@ -364,11 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                                 }
                                 tc::mma_commit(&s_full[x]);
                                 tc::mma_commit(&kv_empty[t % S]);
-                                if (i + 2 == steps) tc::mma_commit(&q_empty);
+                                if (i + 2 == steps) tc::mma_commit(&q_used[x]);
                             }
                         } else if (ok && lane == 0) {
                             tc::mbar_arrive(&kv_empty[t % S]);         // a tile of keys that only the other tile takes
-                            if (i < 0) tc::mbar_arrive(&q_empty);
                         }
                         __syncwarp();
                     }
@@ -438,6 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     tc::tma_load_3d(ring + slot * C::kTile + lh * C::kHalf + lg * box_rows * 128, map, &kv_full[slot], lh * 64,
                                     it.kvh, row);
             };
+            int uses[2] = {0, 0};                                      // queries of each tile loaded (or used up) so far
             if (is_v) {
                 for (int r = 0; ok; ++r) {
                     const Item it = item_at(r, ok);
@@ -451,6 +456,24 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         page = after;
                     }
                     t0 += 2 * total;
+                    // a tile whose queries have done their part: their place takes the gate's inputs, and
+                    // then the outputs on their way to memory
+                    for (int x = 0; x < 2 && ok; ++x) {
+                        if (it.steps(x, tokens) == 0) continue;
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_used[x], (uint32_t)uses[x] & 1u));
+                        ++uses[x];
+                        if (ok && tc::elect_one()) {
+                            if (a.z && it.slot < 0) {
+                                tc::mbar_expect_tx(&z_full[x], (uint32_t)(C::kHalves * tokens * G * 128));
+                                for (int h = 0; h < C::kHalves; ++h)
+                                    tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tz, &z_full[x], h * 64, it.kvh * G,
+                                                    it.q0 + it.tok + x * tokens);
+                            } else {
+                                tc::mbar_arrive(&z_full[x]);
+                            }
+                        }
+                        __syncwarp();
+                    }
                 }
             } else {
                 ItemSource src(a, plan, tokens);
@@ -476,16 +499,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         page = after;
                         if (j > 0 || !ok) continue;
                         // with the first keys, the queries, and the next item for everyone
-                        if (r > 1) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty, (uint32_t)(r - 2) & 1u));
-                        if (ok && tc::elect_one()) {
-                            const int tiles = it.ntok(1, tokens) > 0 ? 2 : 1;
-                            tc::mbar_expect_tx(&q_full, (uint32_t)(tiles * C::kHalves * tokens * G * 128));
-                            for (int x = 0; x < tiles; ++x)
+                        for (int x = 0; x < 2 && ok; ++x) {
+                            if (it.steps(x, tokens) == 0) continue;
+                            if (uses[x] > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[x], (uint32_t)(uses[x] - 1) & 1u));
+                            ++uses[x];
+                            if (ok && tc::elect_one()) {
+                                tc::mbar_expect_tx(&q_full[x], (uint32_t)(C::kHalves * tokens * G * 128));
                                 for (int h = 0; h < C::kHalves; ++h)
-                                    tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tq, &q_full, h * 64, it.kvh * G,
+                                    tc::tma_load_3d(q_smem + x * C::kTile + h * C::kHalf, &tq, &q_full[x], h * 64, it.kvh * G,
                                                     it.q0 + it.tok + x * tokens);
+                            }
+                            __syncwarp();
                         }
-                        __syncwarp();
                         src.next(a, plan, tokens, ahead);
                         put(ahead);
                     }
@@ -510,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         const float sc = fabsf(a.scale) * kLog2e;
         bool ok = true;
         int t0 = 0, done = 0, lasts = 0;                               // ring tiles, steps and last steps before this item
+        int outs = 0, stages = 0;                                      // outputs before it, phases of staged[x]
         for (int r = 0; ok; ++r) {
             Item it = item_at(r, ok);
             if (it.slot == -2) break;
@@ -628,25 +654,23 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             if (!ok) break;
             it = s_item[r % kItems];                      // (again: not kept in registers over the loop)
             item_done(r);
-            const bool live = tok < it.ntok(x, tokens);
+            const int ntok = it.ntok(x, tokens);
+            const bool live = tok < ntok;
             const int64_t at = (((int64_t)it.q0 + it.tok + x * tokens + tok) * a.HQ + it.kvh * G + g) * D;
-            // the gate's inputs, on their way while the last product runs
-            uint4 z[D / 8];
-            const bool gated = a.z && live && it.slot < 0;
-            if (gated) {
-#pragma unroll
-                for (int e = 0; e < D / 8; ++e) z[e] = reinterpret_cast<const uint4*>((const bf16*)a.z + at)[e];
-            }
             if (steps > 0) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + steps - 1) & 1u));
+                // (the queries' place is ours, with the gate's inputs in it)
+                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&z_full[x], (uint32_t)outs & 1u));
                 if (!ok) break;
                 tc::tc_fence_after();
+                ++outs;
             }
             if (it.slot >= 0) {
                 // a piece: the sums as they are, for the join
                 const int64_t pr = (int64_t)it.slot * kSplitRows + x * kRows + row;
                 if (live) plan.part_ml[pr] = make_float2(m, l);
                 if (steps > 0) {
+                    if (warp == 4 * x && lane == 0) tc::mbar_arrive(&q_empty[x]);
                     float4* out = reinterpret_cast<float4*>(plan.part_o + pr * D);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -660,42 +684,86 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         }
                     }
                 }
+            } else if (steps == 0) {
+                // no row of the tile sees a key, though the other tile's do
+                if (live)
+                    for (int c = 0; c < D; c += 8) *reinterpret_cast<uint4*>((bf16*)a.o + at + c) = make_uint4(0, 0, 0, 0);
             } else {
+                // O / sum, gated, as bf16 into shared memory, in the swizzled layout of the tile copies
                 const bool empty = lim < 0;
                 const float inv = empty ? 0.f : 1.0f / l;
-#pragma unroll
+                float bad = 0.f;                       // 0 * y: NaN once a y is not finite
+                uint8_t* stage = q_smem + x * C::kTile + row * 128;
+#pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     float o[32];
-                    if (steps > 0) {
-                        tc::tmem_ld32_raw(to + c, reinterpret_cast<uint32_t*>(o));
-                        tc::tmem_wait_ld();
-                    }
-                    if (live) {
+                    tc::tmem_ld32_raw(to + c, reinterpret_cast<uint32_t*>(o));
+                    tc::tmem_wait_ld();
+                    uint8_t* place = stage + (c >> 6) * C::kHalf;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            o[e] = empty ? 0.f : o[e] * inv;
-                            finite = finite && fabsf(o[e]) <= 3.4028235e38f;
+                    for (int e = 0; e < 4; ++e) {
+                        uint4* p = reinterpret_cast<uint4*>(place + (((((c & 32) >> 3) + e) ^ (row & 7)) << 4));
+                        float y[8];
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            y[k] = empty ? 0.f : o[8 * e + k] * inv;
+                            bad = fmaf(y[k], 0.f, bad);
                         }
-                        if (gated && !empty) {
+                        if (a.z && !empty) {
+                            const uint4 zz = *p;
+                            const uint32_t w[4] = {zz.x, zz.y, zz.z, zz.w};
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const uint4 zz = z[c / 8 + e];
-                                const uint32_t w[4] = {zz.x, zz.y, zz.z, zz.w};
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int j = e * 8 + 2 * k;
-                                    o[j] = gate_out_fast(o[j], __uint_as_float(w[k] << 16));
-                                    o[j + 1] = gate_out_fast(o[j + 1], __uint_as_float(w[k] & 0xffff0000u));
-                                }
+                            for (int k = 0; k < 4; ++k) {
+                                y[2 * k] = gate_out_fast(y[2 * k], __uint_as_float(w[k] << 16));
+                                y[2 * k + 1] = gate_out_fast(y[2 * k + 1], __uint_as_float(w[k] & 0xffff0000u));
                             }
                         }
-                        uint4* out = reinterpret_cast<uint4*>((bf16*)a.o + at + c);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            out[e] = make_uint4(pack_bf16(o[e * 8], o[e * 8 + 1]), pack_bf16(o[e * 8 + 2], o[e * 8 + 3]),
-                                                pack_bf16(o[e * 8 + 4], o[e * 8 + 5]),
-                                                pack_bf16(o[e * 8 + 6], o[e * 8 + 7]));
+                        *p = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
+                                        pack_bf16(y[6], y[7]));
                     }
+                }
+                if (bad != 0.f) finite = false;
+                // out: a whole tile by a tile copy, what is left of a sequence row by row
+                const bool whole = ntok == tokens;
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&staged[x]);
+                if (whole) {
+                    if (warp == 4 * x) {
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)stages & 1u));
+                        if (ok && lane == 0) {
+                            for (int h = 0; h < C::kHalves; ++h)
+                                tc::tma_store_3d(&to_map, q_smem + x * C::kTile + h * C::kHalf, h * 64, it.kvh * G,
+                                                 it.q0 + it.tok + x * tokens);
+                            tc::bulk_commit();
+                            tc::bulk_wait_read<0>();
+                            tc::mbar_arrive(&q_empty[x]);
+                        }
+                        __syncwarp();
+                    }
+                    ++stages;
+                } else {
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)stages & 1u));
+                    if (!ok) break;
+                    constexpr int kLanes = D / 8;      // lanes to a row
+                    const int sub = lane / kLanes, chunk = lane % kLanes;
+#pragma unroll 1
+                    for (int k = sub; k < 32; k += 32 / kLanes) {
+                        const int rk = (warp & 3) * 32 + k, tk_ = rk / G;
+                        if (tk_ >= ntok) break;
+                        const uint4 v = *reinterpret_cast<const uint4*>(q_smem + x * C::kTile + (chunk >> 3) * C::kHalf + rk * 128 +
+                                                                        (((chunk & 7) ^ (rk & 7)) << 4));
+                        const int64_t to_row = ((int64_t)it.q0 + it.tok + x * tokens + tk_) * a.HQ + it.kvh * G + rk - tk_ * G;
+                        *reinterpret_cast<uint4*>((bf16*)a.o + to_row * D + chunk * 8) = v;
+                    }
+                    // (all have read before the place takes the next queries)
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&staged[x]);
+                    if (warp == 4 * x) {
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)(stages + 1) & 1u));
+                        if (ok && lane == 0) tc::mbar_arrive(&q_empty[x]);
+                    }
+                    stages += 2;
                 }
                 if (__any_sync(0xffffffffu, !finite && live) && lane == 0)
                     list_redo(plan, it.n, it.kvh, (it.tok + x * tokens) * G + (warp & 3) * 32,
@@ -706,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             done += steps;
             lasts += steps > 0 && steps == it.total(tokens);
         }
+        if (lane == 0) tc::bulk_wait<0>();             // (the tile copies out are complete)
         if (!ok && lane == 0) s_timeout = 1;
     }
     tc::tc_fence_before();
@@ -799,14 +868,16 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     const int blocks = sms < kSplitGrid ? sms : kSplitGrid;
     e = launch_attn_plan(a, plan, 1, 2 * tokens, blocks, s);
     if (e != cudaSuccess) return e;
-    CUtensorMap tq, tk, tv;
+    CUtensorMap tq, tk, tv, tz, to;
     const int page = 1 << a.kv.page_shift;
     const int box_rows = a.kv.table && page < kKeys ? page : kKeys;
     {
         const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.HQ, (cuuint64_t)a.n_tokens};
         const cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.HQ * D * 2};
         const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)tokens};
-        if (!make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+        if (!make_map(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.q, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_map(&tz, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.z ? a.z : a.q, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_map(&to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.o, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
             return cudaErrorInvalidValue;
     }
     const int64_t kv_rows = a.kv.table ? (int64_t)a.kv.n_pages << a.kv.page_shift : a.n_tokens;
@@ -823,7 +894,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     const int64_t most = (int64_t)plan.max_tiles * a.HKV;
     const int grid = plan.can_split || most > blocks ? blocks : (int)most;
     e = launch_pdl(attn_prefill_kernel<D>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tq, tk,
-                   tv, a, plan, tokens, box_rows);
+                   tv, tz, to, a, plan, tokens, box_rows);
     if (e != cudaSuccess) return e;
     count_launch();
     if (plan.can_split && grid > 1) {
