@@ -19,7 +19,7 @@ namespace {
 __device__ int g_append_error;
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 4;          // tokens per block
+constexpr int kMaxTok = 8;          // tokens per block
 
 template <typename IO>
 struct Chunk {                      // 16 bytes of a head
@@ -98,13 +98,18 @@ __global__ void __launch_bounds__(kThreads) append_kernel(AppendArgs a, int tok_
     __syncthreads();
 
     const int heads = (a.q ? a.HQ : 0) + 2 * a.HKV;
-    const int upd = a.D / (2 * N);              // units per head
-    const int units = nt * heads * upd;
-    for (int u = blockIdx.y * kThreads + tid; u < units; u += kThreads * unit_blocks) {
-        const int c = u % upd;
-        const int th = u / upd;
-        const int t = th / heads;
-        int h = th - t * heads;
+    const int upd = a.D / (2 * N);              // units per head: a power of two, 4 to 16
+    // a thread keeps its unit of a head and steps through the (token, head) pairs
+    const int u0 = blockIdx.y * kThreads + tid, c = u0 % upd, step = kThreads * unit_blocks / upd;
+    int t = u0 / upd / heads, th = u0 / upd - t * heads;
+#pragma unroll 2
+    for (; t < nt; th += step) {
+        while (th >= heads) {
+            th -= heads;
+            ++t;
+        }
+        if (t >= nt) break;
+        int h = th;
         if (s_pos[t] < 0) continue;
         const int64_t tok = t0 + t;
         const IO* src;
