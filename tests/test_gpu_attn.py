@@ -467,6 +467,114 @@ def test_long_cache_offsets():
     assert G.gdn_attn_status() == 0
 
 
+# ---- wide groups, many sequences, gates at their ends -----------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("HQ,HKV", [(100, 1), (130, 1), (258, 2)])
+def test_wide_groups(dtype, HQ, HKV):
+    """Groups that leave a tile one token, and that no tile holds."""
+    torch, G = _torch()
+    g = _gen(61)
+    lens = [9, 1, 40]
+    T = sum(lens)
+    q, k, v = _draw(g, (1, T, HQ, 64), dtype), _draw(g, (1, T, HKV, 64), dtype), _draw(g, (1, T, HKV, 64), dtype)
+    z = _draw(g, q.shape, dtype)
+    o = G.gdn_attn_prefill(q, k, v, cu_seqlens=_i32(_cu(lens)), z=z)
+    c = Cache([700, 3], HKV, 64, 16, dtype, 62)
+    qd = _draw(g, (2, HQ, 64), dtype)
+    od = G.gdn_attn_decode(qd, c.k, c.v, c.table, c.lens)
+    kn, vn = _np(k[0]), _np(v[0])
+    for i, n in enumerate(lens):
+        a, b = _cu(lens)[i], _cu(lens)[i + 1]
+        _check_rows(o[0, a:b], q[0, a:b], kn[a:b], vn[a:b], 0, 0.125, dtype, z[0, a:b], f"sequence {i}",
+                    sorted({0, n // 2, n - 1}))
+    _check_decode(c, qd, od, dtype, None, 0.125)
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_many_short_sequences(dtype):
+    """More sequences than a plan block has threads, most of them of a few tokens, some empty."""
+    torch, G = _torch()
+    g = _gen(63)
+    r = np.random.default_rng(5)
+    new = r.integers(0, 9, 1500).tolist()
+    new[1000] = 300
+    past = r.integers(0, 40, 1500).tolist()
+    totals = [n + p for n, p in zip(new, past)]
+    c = Cache(totals, 1, 64, 16, dtype, 64)
+    T, cu = sum(new), _cu(new)
+    q, k, v = _draw(g, (T, 2, 64), dtype), _draw(g, (T, 1, 64), dtype), _draw(g, (T, 1, 64), dtype)
+    qo = G.gdn_attn_append(q, k, v, c.k, c.v, c.table, c.lens, cu_seqlens=_i32(cu))
+    assert torch.equal(qo, q)                                # no rotation
+    o = G.gdn_attn_prefill_paged(qo, c.k, c.v, c.table, c.lens, _i32(cu))
+    whole = G.gdn_attn_prefill(q[None], k[None], v[None], cu_seqlens=_i32(cu))[0]
+    kn, vn = _np(k), _np(v)
+    for i in [0, 1, 2, 999, 1000, 1001, 1023, 1024, 1025, 1499, *r.integers(0, 1500, 40).tolist()]:
+        a, b = cu[i], cu[i + 1]
+        rows = sorted({0, new[i] // 2, new[i] - 1}) if new[i] else []
+        kc, vc = c.seq(i) if totals[i] else (None, None)
+        _check_rows(o[a:b], q[a:b], kc, vc, past[i], 0.125, dtype, None, f"paged {i}", rows)
+        _check_rows(whole[a:b], q[a:b], kn[a:b], vn[a:b], 0, 0.125, dtype, None, f"whole {i}", rows)
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gate_at_its_ends(dtype):
+    """Gates of infinities are 0 and 1, very negative ones 0; a NaN gate is a NaN there only."""
+    torch, G = _torch()
+    g = _gen(65)
+    c = Cache([500], 1, 128, 64, dtype, 66)
+    for n in (1, 130):
+        q = _draw(g, (n, 2, 128), dtype)
+        cu, lens = _i32([0, n]), c.lens
+        plain = _np(G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, lens, cu))
+        z = torch.zeros_like(q)
+        z[..., 0], z[..., 1], z[..., 2], z[..., 3], z[..., 4] = float("inf"), -float("inf"), -300.0, 300.0, float("nan")
+        outs = [G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, lens, cu, z=z)]
+        if n == 1:
+            outs.append(G.gdn_attn_decode(q, c.k, c.v, c.table, lens, z=z))
+        for o in outs:
+            o = _np(o)
+            assert np.isnan(o[..., 4]).all() and np.isfinite(np.delete(o, 4, axis=-1)).all()
+            assert not o[..., 1].any() and not o[..., 2].any()
+            tol = 3 * R.HALF_STEP[dtype] + 64 * R.U             # both sides rounded, and their sums' order
+            for col, f in ((0, 1.0), (3, 1.0), (5, 0.5)):
+                assert (np.abs(o[..., col] - f * plain[..., col]) <= tol * (np.abs(plain[..., col]) + 0.2)).all()
+    assert G.gdn_attn_status() == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured graphs over one workspace, replayed in turn on one stream."""
+    torch, G = _torch()
+    g = _gen(67)
+    new, past = [33, 5], [5000, 77]
+    totals = [n + p for n, p in zip(new, past)]
+    c = Cache(totals, 2, 128, 64, "bf16", 68)
+    T, cu = sum(new), _i32(_cu(new))
+    q = [_draw(g, (T, 8, 128), "bf16") for _ in range(2)]
+    qd = [_draw(g, (2, 8, 128), "bf16") for _ in range(2)]
+    n = max(G.attn_prefill_workspace_bytes(T, 2, 8, 2, 128, 1), G.attn_decode_workspace_bytes(2, 8, 2, 128, 1))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    step = lambda i: (G.gdn_attn_prefill_paged(q[i], c.k, c.v, c.table, c.lens, cu, workspace=ws),
+                      G.gdn_attn_decode(qd[i], c.k, c.v, c.table, c.lens, workspace=ws))
+    want = [step(i) for i in range(2)]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for i in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got.append(step(i))
+        graphs.append(graph)
+    ws.fill_(255)                                            # what a workspace holds does not matter
+    for _ in range(3):
+        for i in (0, 1, 1, 0):
+            for o in got[i]:
+                o.zero_()
+            graphs[i].replay()
+            assert all(torch.equal(a, b) for a, b in zip(got[i], want[i]))
+    assert G.gdn_attn_status() == 0
+
+
 # ---- bad tables (checked by paged.cuh, whose arithmetic test_attn_ref.py checks) --------------
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_bad_tables_are_reported_and_stay_contained(dtype):
