@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         }
         for (int x = 0; x < 2; ++x) {
             tc::mbar_init(&q_full[x], 1);
-            tc::mbar_init(&q_empty[x], 1);
+            tc::mbar_init(&q_empty[x], 4);
             tc::mbar_init(&q_used[x], 1);
             tc::mbar_init(&z_full[x], 1);
             tc::mbar_init(&staged[x], 4);
@@ -579,6 +579,21 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     if (i > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
                     tc::tc_fence_after();
                 };
+                if (clear_from - j0 < kKeys) {
+                    // Values that no row of the block sees may be anything: clear them, every warp its
+                    // share, whatever rows it has.  (The MMA warp, which sees every copy land in turn,
+                    // tells when they are there.)
+                    const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&v_last[x], (uint32_t)lasts & 1u));
+                    if (!ok) break;
+                    uint8_t* v = ring + slot * C::kTile;
+                    const int first = clear_from - j0;
+                    for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
+                        const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
+                        *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc::fence_async_smem();
+                }
                 bool stand = false;
                 if (!masked) {
                     const float sum = weights<false, C::kPoly>(s, sc, m, 0, tp, free);
@@ -628,20 +643,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             }
                         }
                     }
-                    if (clear_from - j0 < kKeys) {
-                        // values that no row of the block sees may be anything: clear them
-                        // (the MMA warp, which sees every copy land in turn, tells when they are there)
-                        const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&v_last[x], (uint32_t)lasts & 1u));
-                        if (!ok) break;
-                        uint8_t* v = ring + slot * C::kTile;
-                        const int first = clear_from - j0;
-                        for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
-                            const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
-                            *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        tc::fence_async_smem();
-                    }
                     const float base = m == -INFINITY ? 0.f : m;
                     l += weights<true, false>(s, sc, base, lim - j0, tp, free);
                 }
@@ -670,7 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 const int64_t pr = (int64_t)it.slot * kSplitRows + x * kRows + row;
                 if (live) plan.part_ml[pr] = make_float2(m, l);
                 if (steps > 0) {
-                    if (warp == 4 * x && lane == 0) tc::mbar_arrive(&q_empty[x]);
+                    if (lane == 0) tc::mbar_arrive(&q_empty[x]);
                     float4* out = reinterpret_cast<float4*>(plan.part_o + pr * D);
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
@@ -737,11 +738,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                                                  it.q0 + it.tok + x * tokens);
                             tc::bulk_commit();
                             tc::bulk_wait_read<0>();
-                            tc::mbar_arrive(&q_empty[x]);
                         }
                         __syncwarp();
                     }
-                    ++stages;
                 } else {
                     ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)stages & 1u));
                     if (!ok) break;
@@ -756,15 +755,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         const int64_t to_row = ((int64_t)it.q0 + it.tok + x * tokens + tk_) * a.HQ + it.kvh * G + rk - tk_ * G;
                         *reinterpret_cast<uint4*>((bf16*)a.o + to_row * D + chunk * 8) = v;
                     }
-                    // (all have read before the place takes the next queries)
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&staged[x]);
-                    if (warp == 4 * x) {
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)(stages + 1) & 1u));
-                        if (ok && lane == 0) tc::mbar_arrive(&q_empty[x]);
-                    }
-                    stages += 2;
                 }
+                ++stages;
+                // The place is free for the next queries once every warp has said so: each has then seen
+                // its phase of z_full (a warp that is still to look at one must not miss two), and read
+                // its rows, or, the first warp, seen the tile copy read them.
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&q_empty[x]);
                 if (__any_sync(0xffffffffu, !finite && live) && lane == 0)
                     list_redo(plan, it.n, it.kvh, (it.tok + x * tokens) * G + (warp & 3) * 32,
                               min(32, tokens * G - (warp & 3) * 32));

@@ -322,6 +322,9 @@ def test_prefill_back_to_back(D, HQ, HKV):
         a, b = cu[i], cu[i + 1]
         _check_rows(outs[-1][0, a:b], q[0, a:b], kn[a:b], vn[a:b], 0, D ** -0.5, "bf16", None, f"sequence {i}",
                     _some(lens[i], i, 10))
+    for _ in range(4000):
+        G.gdn_attn_prefill(q, k, v, cu_seqlens=cud, o=outs[1], workspace=ws)
+    assert G.gdn_attn_status() == 0 and torch.equal(outs[1], outs[0])
 
 
 def test_paged_back_to_back_split():
@@ -334,16 +337,20 @@ def test_paged_back_to_back_split():
     q = _draw(g, (sum(new), 32, 128), "bf16")
     z = _draw(g, q.shape, "bf16")
     cud = _i32(_cu(new))
-    outs = [torch.empty_like(q) for _ in range(200)]
-    for o in outs:
-        G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cud, z=z, o=o)
-    assert G.gdn_attn_status() == 0
-    for i, o in enumerate(outs):
-        assert torch.equal(o, outs[0]), i
+    ws = torch.empty(G.attn_prefill_workspace_bytes(sum(new), len(new), 32, 8, 128, 1), dtype=torch.uint8, device="cuda")
+    call = lambda o: G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cud, z=z, o=o, workspace=ws)
+    outs = [call(torch.empty_like(q)) for _ in range(200)]
+    o = torch.empty_like(q)
+    for gated in (z, None):             # thousands of launches: a wait that is rarely missed shows
+        for _ in range(4000):
+            G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cud, z=gated, o=o, workspace=ws)
+        assert G.gdn_attn_status() == 0
+    for i, x in enumerate(outs):
+        assert torch.equal(x, outs[0]), i
     for i, n in enumerate(new):
         kn, vn = c.seq(i)
         a = _cu(new)[i]
-        _check_rows(o[a:a + n], q[a:a + n], kn, vn, past[i], 128 ** -0.5, "bf16", z[a:a + n], f"sequence {i}",
+        _check_rows(outs[0][a:a + n], q[a:a + n], kn, vn, past[i], 128 ** -0.5, "bf16", z[a:a + n], f"sequence {i}",
                     sorted({0, n // 2, n - 1}))
 
 
@@ -380,6 +387,21 @@ def test_prefill_paged(dtype, D, HQ, HKV, page, new, past, gate):
                     f"sequence {i}", _some(n, i, 10))
     assert (o[T:] == 7.0).all()
     assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("new,past,page", [([130], [129], 16), ([3, 1], [130, 12000], 16), ([20, 64], [7000, 2500], 128),
+                                           ([33, 257], [9001, 0], 64)])
+def test_slots_past_the_contexts_cost_nothing(new, past, page):
+    """Slots that no sequence holds (NaN here) are cleared on the way, not found in the outputs: the
+    list of rows to do again (its length is word 1 of the workspace) stays empty."""
+    torch, G = _torch()
+    g = _gen(24)
+    for D in (64, 128):
+        c = Cache([n + p for n, p in zip(new, past)], 2, D, page, "bf16", 25)
+        q = _draw(g, (sum(new), 8, D), "bf16")
+        ws = torch.zeros(G.attn_prefill_workspace_bytes(sum(new), len(new), 8, 2, D, 1), dtype=torch.uint8, device="cuda")
+        o = G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, _i32(_cu(new)), workspace=ws)
+        assert torch.isfinite(o).all() and ws[4:8].view(torch.int32).item() == 0
 
 
 # ---- decode -----------------------------------------------------------------------------
