@@ -124,7 +124,8 @@ gdn_status gdn_attn_append(const void* q, const void* k, const void* v, gdn_dtyp
         (rotary_dim > 0 && !inv_freq))
         return GDN_ERR_NULL;
     const size_t es = esize(io_dtype);
-    if (!all_aligned({q, k, v, inv_freq, cu_seqlens, kv_lens, block_table, q_out, k_cache, v_cache})) return GDN_ERR_ALIGN;
+    if (!all_aligned({q, k, v, inv_freq, cu_seqlens, kv_lens, block_table, q_out, k_cache, v_cache}))
+        return GDN_ERR_ALIGN;
     if ((q && q_stride * es % 16) || k_stride * es % 16 || v_stride * es % 16) return GDN_ERR_ALIGN;
     const size_t n1 = (size_t)n_tokens - 1;
     const Range rq{q, (n1 * q_stride + (size_t)HQ * D) * es}, rk{k, (n1 * k_stride + (size_t)HKV * D) * es};

@@ -286,7 +286,8 @@ cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s) {
     const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 0, G, kM, 0, 0);
     cudaError_t e = launch_attn_plan(a, plan, G, kM, 0, s);
     if (e != cudaSuccess) return e;
-    if (a.bf16) return a.D == 128 ? launch_cc<__nv_bfloat16, 128>(a, plan, s) : launch_cc<__nv_bfloat16, 64>(a, plan, s);
+    if (a.bf16)
+        return a.D == 128 ? launch_cc<__nv_bfloat16, 128>(a, plan, s) : launch_cc<__nv_bfloat16, 64>(a, plan, s);
     return a.D == 128 ? launch_cc<float, 128>(a, plan, s) : launch_cc<float, 64>(a, plan, s);
 }
 

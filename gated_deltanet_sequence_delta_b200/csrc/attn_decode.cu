@@ -583,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             from_start = cur.tile == 0;
             if constexpr (sizeof(IO) == 4) {
                 // the rows' queries for every warp (rows past the group: zeros)
-                for (int i = tid; i < R * D; i += kConsumers) sq[i] = i < rows * D ? ((const float*)a.q)[qrow + i] : 0.f;
+                for (int i = tid; i < R * D; i += kConsumers)
+                    sq[i] = i < rows * D ? ((const float*)a.q)[qrow + i] : 0.f;
                 tc::named_bar(1, kConsumers);
             }
             st.start((const IO*)a.q + qrow, rows, sq);
@@ -615,7 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 for (int k = 0; k < 8; ++k) {
                     const float* pk = p + k * R * (D + 4);
                     // a warp that took no key: m = -inf, l = 0, o = 0
-                    const float f = pk[D] == -INFINITY && pk[D + 1] == 0.f ? 0.f : exp2f(pk[D] - (m == -INFINITY ? 0.f : m));
+                    const bool none = pk[D] == -INFINITY && pk[D + 1] == 0.f;
+                    const float f = none ? 0.f : exp2f(pk[D] - (m == -INFINITY ? 0.f : m));
                     const float4 y = *reinterpret_cast<const float4*>(pk + c);
                     if (f != 0.f || pk[D + 1] != 0.f) {
                         l = fmaf(f, pk[D + 1], l);
@@ -727,7 +729,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return e;
     // one block per SM, fewer where the longest contexts the tables can hold have fewer tiles
-    const int64_t most = (int64_t)a.n_seqs * a.HKV * hb * ((((int64_t)a.kv.max_pages << a.kv.page_shift) + C::KT - 1) / C::KT);
+    const int64_t longest = (((int64_t)a.kv.max_pages << a.kv.page_shift) + C::KT - 1) / C::KT;
+    const int64_t most = (int64_t)a.n_seqs * a.HKV * hb * longest;
     int grid = sms < kMaxGrid ? sms : kMaxGrid;
     if (most < grid) grid = most > 0 ? (int)most : 1;
     CUtensorMap tk, tv;

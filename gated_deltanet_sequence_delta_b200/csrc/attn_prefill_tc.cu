@@ -182,7 +182,8 @@ struct Item {
         return max(min((end(x, tokens) + kKeys - 1) / kKeys, s1) - s0, 0);
     }
     __device__ __forceinline__ int total(int tokens) const { return max(steps(0, tokens), steps(1, tokens)); }
-    __device__ __forceinline__ int first(int tokens) const { return steps(0, tokens) > 0 ? 0 : 1; }   // tile of its first step
+    // the tile of its first step
+    __device__ __forceinline__ int first(int tokens) const { return steps(0, tokens) > 0 ? 0 : 1; }
 };
 
 // (Rows of a bad table may be listed twice: never past the list's end.)
@@ -267,8 +268,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     using C = Cfg<D>;
     constexpr int S = C::kRing;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t q_full[2], q_empty[2], q_used[2], z_full[2], staged[2], kv_full[S], kv_empty[S], s_full[2], turn[2], p_full[2], pv_done[2],
-        v_last[2], drain[2], item_full[kItems], item_empty[kItems];
+    // q_full, q_used, z_full, q_empty: a tile's place for queries holds them, is done with, holds the
+    // gate's inputs (or is free for the outputs), is free; staged: the outputs are in it
+    __shared__ __align__(8) uint64_t q_full[2], q_used[2], z_full[2], staged[2], q_empty[2];
+    // s_full: scores formed; turn: S is this tile's to fill; p_full: weights written; pv_done: their
+    // product has read them; v_last: the item's last values are there
+    __shared__ __align__(8) uint64_t s_full[2], turn[2], p_full[2], pv_done[2], v_last[2];
+    __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], item_full[kItems], item_empty[kItems], drain[2];
     __shared__ Item s_item[kItems];
     __shared__ uint32_t s_tmem;
     __shared__ int s_timeout;
@@ -316,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     // the item ring's reader side: item r, or slot -2 past the last one (or after an expired wait)
     auto item_at = [&](int r, bool& ok) {
         Item it;
-        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&item_full[r % kItems], (uint32_t)(r / kItems) & 1u));
+        if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&item_full[r % kItems], (uint32_t)(r / kItems) & 1u));
         it = s_item[r % kItems];
         if (!ok) it.slot = -2;
         return it;
@@ -335,12 +341,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const uint32_t neg = a.scale < 0.f ? 1u << 13 : 0u;        // -Q: scores of a negative scale
             const uint32_t id_s = tc::idesc_bf16(128, kKeys, 0, 0) | neg, id_o = tc::idesc_bf16(128, D, 0, 1);
             const uint64_t qd = tc::desc_sw128(tc::smem_u32(q_smem + x * C::kTile), 0, 1024);
-            const uint64_t kd = tc::desc_sw128(tc::smem_u32(ring), 0, 1024), vd = tc::desc_sw128(tc::smem_u32(ring), C::kHalf, 1024);
+            const uint64_t kd = tc::desc_sw128(tc::smem_u32(ring), 0, 1024);
+            const uint64_t vd = tc::desc_sw128(tc::smem_u32(ring), C::kHalf, 1024);
             bool ok = true;
             int t0 = 0, items = 0, loads = 0, mine = 0;                // ring tiles, items, queries and steps before this item
             int turns = -1;                                            // phases of turn[x] taken
             auto wait = [&](uint64_t* bar, int phase) {
-                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(bar, (uint32_t)phase & 1u));
+                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(bar, (uint32_t)phase & 1u));
             };
             auto wait_kv = [&](int t) { wait(&kv_full[t % S], t / S); };
             for (int r = 0; ok; ++r) {
@@ -403,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             // every arrival of the commits above has landed before the block leaves
             if (tc::elect_one()) tc::mma_commit(&drain[x]);
             __syncwarp();
-            if (!tc::mbar_wait(&drain[x], 0) || !ok) s_timeout = 1;
+            if (!tc::mbar_wait_short(&drain[x], 0) || !ok) s_timeout = 1;
         } else {
             // ---- loads: warp 10 the items, queries and keys, warp 11 the values ------------------
             // The ring takes K(0), K(1), V(0), K(2), V(1), ..., V(last) of an item.  (Its slots pass
@@ -434,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             atomicMax(&g_attn_tc_error, GDN_DEVERR_PAGE);
                     }
                 }
-                if (t >= S) ok = __all_sync(0xffffffffu, tc::mbar_wait(&kv_empty[slot], (uint32_t)((t / S) & 1) ^ 1u));
+                if (t >= S) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&kv_empty[slot], (uint32_t)((t / S) & 1) ^ 1u));
                 if (!ok) return;
                 if (lane == 0) tc::mbar_expect_tx(&kv_full[slot], C::kTile);
                 __syncwarp();
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     // then the outputs on their way to memory
                     for (int x = 0; x < 2 && ok; ++x) {
                         if (it.steps(x, tokens) == 0) continue;
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_used[x], (uint32_t)uses[x] & 1u));
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&q_used[x], (uint32_t)uses[x] & 1u));
                         ++uses[x];
                         if (ok && tc::elect_one()) {
                             if (a.z && it.slot < 0) {
@@ -480,7 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 Item it, ahead;
                 int r = 0;
                 auto put = [&](const Item& x) {                        // to the other roles
-                    if (r >= kItems) ok = __all_sync(0xffffffffu, tc::mbar_wait(&item_empty[r % kItems], (uint32_t)(r / kItems - 1) & 1u));
+                    if (r >= kItems) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&item_empty[r % kItems], (uint32_t)(r / kItems - 1) & 1u));
                     if (ok && lane == 0) {
                         s_item[r % kItems] = x;
                         tc::mbar_arrive(&item_full[r % kItems]);
@@ -501,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         // with the first keys, the queries, and the next item for everyone
                         for (int x = 0; x < 2 && ok; ++x) {
                             if (it.steps(x, tokens) == 0) continue;
-                            if (uses[x] > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&q_empty[x], (uint32_t)(uses[x] - 1) & 1u));
+                            if (uses[x] > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&q_empty[x], (uint32_t)(uses[x] - 1) & 1u));
                             ++uses[x];
                             if (ok && tc::elect_one()) {
                                 tc::mbar_expect_tx(&q_full[x], (uint32_t)(C::kHalves * tokens * G * 128));
@@ -520,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             }
             if (!ok) {       // an expired wait: give the copies under way time to land
                 if (lane == 0) s_timeout = 1;
-                for (int i = 0; i < S; ++i) tc::mbar_wait(&kv_full[i], 0, 1000000);
+                for (int i = 0; i < S; ++i) tc::mbar_wait_short(&kv_full[i], 0, 1000000);
             }
         }
     } else {
@@ -550,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             float m = -INFINITY, l = 0.f;
             bool finite = true;
             for (int i = 0; i < steps; ++i) {
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&s_full[x], (uint32_t)(done + i) & 1u));
+                ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&s_full[x], (uint32_t)(done + i) & 1u));
                 if (!ok) break;
                 tc::tc_fence_after();
                 float s[128];
@@ -576,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 // They stand if no row's sum says that it should have moved.
                 const bool masked = __any_sync(0xffffffffu, j0 + kKeys - 1 > lim || (m == -INFINITY && lim != INT32_MAX));
                 auto free = [&] {                        // the last step's product has read P
-                    if (i > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
+                    if (i > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
                     tc::tc_fence_after();
                 };
                 if (clear_from - j0 < kKeys) {
@@ -584,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     // share, whatever rows it has.  (The MMA warp, which sees every copy land in turn,
                     // tells when they are there.)
                     const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&v_last[x], (uint32_t)lasts & 1u));
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&v_last[x], (uint32_t)lasts & 1u));
                     if (!ok) break;
                     uint8_t* v = ring + slot * C::kTile;
                     const int first = clear_from - j0;
@@ -629,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                             m = mx;
                         }
                         if (i > 0) {
-                            ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
+                            ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
                             if (!ok) break;
                             tc::tc_fence_after();
 #pragma unroll 1
@@ -659,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             const bool live = tok < ntok;
             const int64_t at = (((int64_t)it.q0 + it.tok + x * tokens + tok) * a.HQ + it.kvh * G + g) * D;
             if (steps > 0) {
-                ok = __all_sync(0xffffffffu, tc::mbar_wait(&pv_done[x], (uint32_t)(done + steps - 1) & 1u));
+                ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&pv_done[x], (uint32_t)(done + steps - 1) & 1u));
                 // (the queries' place is ours, with the gate's inputs in it)
-                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&z_full[x], (uint32_t)outs & 1u));
+                if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&z_full[x], (uint32_t)outs & 1u));
                 if (!ok) break;
                 tc::tc_fence_after();
                 ++outs;
@@ -731,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (lane == 0) tc::mbar_arrive(&staged[x]);
                 if (whole) {
                     if (warp == 4 * x) {
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)stages & 1u));
+                        ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&staged[x], (uint32_t)stages & 1u));
                         if (ok && lane == 0) {
                             for (int h = 0; h < C::kHalves; ++h)
                                 tc::tma_store_3d(&to_map, q_smem + x * C::kTile + h * C::kHalf, h * 64, it.kvh * G,
@@ -742,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         __syncwarp();
                     }
                 } else {
-                    ok = __all_sync(0xffffffffu, tc::mbar_wait(&staged[x], (uint32_t)stages & 1u));
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&staged[x], (uint32_t)stages & 1u));
                     if (!ok) break;
                     constexpr int kLanes = D / 8;      // lanes to a row
                     const int sub = lane / kLanes, chunk = lane % kLanes;

@@ -85,6 +85,31 @@ __device__ __forceinline__ bool mbar_wait_spin(uint64_t* bar, uint32_t parity, u
     return mbar_wait(bar, parity, timeout_ns);
 }
 
+// The same bounded wait in a few instructions, for kernels whose code holds many: each poll may
+// suspend for up to a microsecond, and the clock is read once in 16.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, uint64_t timeout_ns = 2000000000ull) {
+    const uint32_t addr = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (int i = 0;; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity), "r"(1000)
+            : "memory");
+        if (done) return true;
+        if ((i & 15) == 15) {
+            const uint64_t t = globaltimer_ns();
+            if (!t0)
+                t0 = t;
+            else if (t - t0 > timeout_ns)
+                return false;
+        }
+    }
+}
+
 // ---- thread-block clusters --------------------------------------------------------
 // All threads of every CTA of the cluster; orders the shared memory of each before the
 // others' later accesses to it.
