@@ -73,7 +73,7 @@ struct AttnPlan {
     int4* desc;                 // split plans, [block]: {tile, key-value head, first, last block} of the one the block began
                                 // inside, as the first that did; or tile = -1
     float2* part_ml;            // pieces of tiles that blocks share: [block][2][256] (maximum, sum), and
-    float* part_o;              // [block][2][256][D]
+    float* part_o;              // outputs, [block][2][tile of 128 rows][D / 4][128][4]
     int max_tiles, max_redo;
     bool can_split;
     size_t bytes;

@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 if (live) plan.part_ml[pr] = make_float2(m, l);
                 if (steps > 0) {
                     if (lane == 0) tc::mbar_arrive(&q_empty[x]);
-                    float4* out = reinterpret_cast<float4*>(plan.part_o + pr * D);
+                    // [4 columns][row]: a warp's rows lie together in every store
+                    float4* out = reinterpret_cast<float4*>(plan.part_o) + (pr - row) * (D / 4) + row;
 #pragma unroll 1
                     for (int c = 0; c < D; c += 16) {
                         float o[16];
@@ -688,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         if (live) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                out[c / 4 + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                                out[(c / 4 + e) * kRows] =
+                                    make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
                         }
                     }
                 }
@@ -789,40 +791,44 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
 }
 
 // Joins the pieces of a split plan.  Block (c - 1, y): rows 16 y .. 16 y + 15 of the (tile, head) that
-// block c of the main kernel left to it, two rows a warp, kBatch pieces' loads in flight.
-constexpr int kJoinThreads = 256, kBatch = 4;
+// block c of the main kernel left to it; a thread one row and D / 64 chunks of four columns (the pieces
+// lie as [4 columns][row]), kBatch pieces' loads in flight.  The outputs go through shared memory, so
+// that gate inputs and outputs are read and written 16 bytes at a time along the rows.
+constexpr int kJoinThreads = 256, kJoinRows = 16, kBatch = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a, AttnPlan plan, int tokens) {
-    constexpr int E = D / 32;
+    constexpr int NC = D / 64, kStride = D + 4;
+    __shared__ float s_y[kJoinRows * kStride];
     tc::grid_dependency_sync();
     const int c = blockIdx.x + 1;
     if (c >= plan.counts[3]) return;
     const int4 d = plan.desc[c];
     if (d.x < 0) return;
     const PlanTile t = plan.tiles[d.x];
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, G = a.HQ / a.HKV, h = d.y;
-    const int r0 = blockIdx.y * 16, x = r0 / kRows;
+    const int tid = threadIdx.x, G = a.HQ / a.HKV, h = d.y;
+    const int r0 = blockIdx.y * kJoinRows, x = r0 / kRows, tr0 = r0 - x * kRows;
     const int tok0 = (t.index * 2 + x) * tokens;            // the half's first token
-    if (tok0 + (r0 - x * kRows) / G >= t.n_q) return;       // no row here
+    const int rows = min(tokens, t.n_q - tok0) * G - tr0;   // the half's rows from r0 on
+    if (rows <= 0) return;
+    const int64_t to0 = ((int64_t)t.q0 + tok0) * a.HQ + (int64_t)h * G;
     bool finite = true;
+    {
+        const int row = tid % kJoinRows, chunk = tid / kJoinRows;
+        float m = -INFINITY, l = 0.f;
+        float4 o[NC];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int r = r0 + 2 * w + i, tr = r - x * kRows, tok = tok0 + tr / G;
-        if (tr >= tokens * G || tok >= t.n_q) continue;
-        float m = -INFINITY, l = 0.f, o[E] = {};
-        for (int b0 = d.z; b0 <= d.w; b0 += kBatch) {
+        for (int i = 0; i < NC; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b0 = row < rows ? d.z : d.w + 1; b0 <= d.w; b0 += kBatch) {
             float2 ml[kBatch];
-            float y[kBatch][E];
+            float4 y[kBatch][NC];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 const int b = min(b0 + k, d.w);                // (past the end: read again, not used)
-                const int64_t at = ((int64_t)b * 2 + (b == d.z ? 1 : 0)) * kSplitRows + r;
-                ml[k] = plan.part_ml[at];
-                const float* p = plan.part_o + at * D + lane * E;
-                if constexpr (E == 4)
-                    *reinterpret_cast<float4*>(y[k]) = *reinterpret_cast<const float4*>(p);
-                else
-                    *reinterpret_cast<float2*>(y[k]) = *reinterpret_cast<const float2*>(p);
+                const int64_t half = ((int64_t)b * 2 + (b == d.z ? 1 : 0)) * kSplitRows + x * kRows;
+                ml[k] = plan.part_ml[half + tr0 + row];
+                const float4* p = reinterpret_cast<const float4*>(plan.part_o) + half * (D / 4) + tr0 + row;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) y[k][i] = p[(chunk + i * 16) * kRows];
             }
             float mn = m;
 #pragma unroll
@@ -832,7 +838,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a
             m = mn;
             l *= g;
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] *= g;
+            for (int i = 0; i < NC; ++i) o[i] = make_float4(o[i].x * g, o[i].y * g, o[i].z * g, o[i].w * g);
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 // (a piece in which the row sees no key has no sums, whatever lies there)
@@ -840,24 +846,50 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a
                 const float f = exp2_sfu(ml[k].x - base);
                 l = fmaf(f, ml[k].y, l);
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = fmaf(f, y[k][e], o[e]);
+                for (int i = 0; i < NC; ++i) {
+                    o[i].x = fmaf(f, y[k][i].x, o[i].x);
+                    o[i].y = fmaf(f, y[k][i].y, o[i].y);
+                    o[i].z = fmaf(f, y[k][i].z, o[i].z);
+                    o[i].w = fmaf(f, y[k][i].w, o[i].w);
+                }
             }
         }
-        const bool empty = t.n_kv - t.n_q + tok < 0;
-        const int64_t to = (((int64_t)t.q0 + tok) * a.HQ + h * G + tr % G) * D + lane * E;
+        if (row < rows) {
+            const bool empty = t.n_kv - t.n_q + tok0 + (tr0 + row) / G < 0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            float v = empty ? 0.f : o[e] / l;
-            finite = finite && fabsf(v) <= 3.4028235e38f;
-            if (a.z && !empty) v = gate_out_fast(v, __bfloat162float(((const bf16*)a.z)[to + e]));
-            ((bf16*)a.o)[to + e] = __float2bfloat16_rn(v);
+            for (int i = 0; i < NC; ++i) {
+                const float4 v = empty ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                       : make_float4(o[i].x / l, o[i].y / l, o[i].z / l, o[i].w / l);
+                // 0 * v: NaN once a v is not finite
+                const float bad = fmaf(v.x, 0.f, fmaf(v.y, 0.f, fmaf(v.z, 0.f, v.w * 0.f)));
+                finite = finite && bad == 0.f;
+                *reinterpret_cast<float4*>(s_y + row * kStride + (chunk + i * 16) * 4) = v;
+            }
         }
     }
-    // (rows are listed as the (token, head) rows of the sequence)
-    if (__syncthreads_or(!finite) && tid == 0) {
-        const int tr = r0 - x * kRows;
-        list_redo(plan, t.n, h, tok0 * G + tr, min(16, tokens * G - tr));
+    const bool redo = __syncthreads_or(!finite);
+    for (int u = tid; u < kJoinRows * (D / 8); u += kJoinThreads) {
+        const int row = u / (D / 8), col = u % (D / 8) * 8, tr = tr0 + row;
+        if (row >= rows) break;
+        const int64_t to = (to0 + (int64_t)(tr / G) * a.HQ + tr % G) * D + col;
+        const float* y = s_y + row * kStride + col;
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = y[e];
+        if (a.z && t.n_kv - t.n_q + tok0 + tr / G >= 0) {
+            const uint4 zz = *reinterpret_cast<const uint4*>((const bf16*)a.z + to);
+            const uint32_t w[4] = {zz.x, zz.y, zz.z, zz.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[2 * e] = gate_out_fast(v[2 * e], __uint_as_float(w[e] << 16));
+                v[2 * e + 1] = gate_out_fast(v[2 * e + 1], __uint_as_float(w[e] & 0xffff0000u));
+            }
+        }
+        *reinterpret_cast<uint4*>((bf16*)a.o + to) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     }
+    // (rows are listed as the (token, head) rows of the sequence)
+    if (redo && tid == 0) list_redo(plan, t.n, h, tok0 * G + tr0, min(kJoinRows, tokens * G - tr0));
 }
 
 template <int D>
@@ -902,7 +934,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     count_launch();
     if (plan.can_split && grid > 1) {
-        e = launch_pdl(attn_join_rows_kernel<D>, dim3((unsigned)(grid - 1), kSplitRows / 16), dim3(kJoinThreads), 0, s, a,
+        e = launch_pdl(attn_join_rows_kernel<D>, dim3((unsigned)(grid - 1), kSplitRows / kJoinRows), dim3(kJoinThreads), 0, s, a,
                        plan, tokens);
         if (e != cudaSuccess) return e;
         count_launch();

@@ -2,7 +2,9 @@
  * gdn.h -- C ABI of the Gated DeltaNet core for NVIDIA B200 (sm_100a).
  *
  * The library computes the gated delta rule in two modes, chunked prefill and
- * a one-token recurrent decode step, plus the gate computation that feeds both.
+ * a one-token recurrent decode step, plus the gate computation that feeds both;
+ * and, for the attention layers of the same hybrid stack, causal grouped attention
+ * with its paged key-value cache (gdn_attn_*, described in front of those calls).
  *
  *   Gates ("Gated DeltaNet ... Qwen3-next" page, section 2.1, gate code):
  *       beta = sigmoid(b),  g = -exp(A_log) * softplus(a + dt_bias),  alpha = exp(g)
@@ -16,7 +18,8 @@
  * Conventions shared by every call:
  *   - All tensor pointers are DEVICE memory, allocated, owned and freed by the
  *     caller.  The library never allocates, frees or synchronises, except in
- *     gdn_chunk_prefill_status(), which synchronises the given stream.
+ *     gdn_chunk_prefill_status(), which synchronises the given stream, and the
+ *     other status calls, which synchronise the device.
  *   - Every call is asynchronous on `stream` (a cudaStream_t; NULL = legacy
  *     default stream).  Arguments are validated on the host before anything is
  *     launched; a non-GDN_OK return means nothing was launched.
