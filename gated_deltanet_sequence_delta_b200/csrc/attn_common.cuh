@@ -62,7 +62,7 @@ struct PlanTile {
     int n, index;               // sequence, which of its tiles
     int q0, n_q, n_kv;          // the sequence's rows (seq_rows)
     int steps;                  // key steps of 128 (kept by the tensor-core path), at least 1
-    int before;                 // steps of the tiles before it in the list (split plans only)
+    int before;                 // units of the tiles before it in the list (split plans only)
     int pad;
 };
 struct AttnPlan {
@@ -80,6 +80,11 @@ struct AttnPlan {
 };
 constexpr int kSplitGrid = 160;     // blocks that a split plan has room for
 constexpr int kSplitRows = 256;
+// A split plan counts work in units: a (tile, key-value head)'s steps and, in front of them, its own
+// start and end (queries in, outputs out, a step's chain that nothing overlaps) as this many steps
+// (2048 tokens, 16 heads over 4: 79 us at 0, 54 at 2, 49 at 3, 50 at 4, 52 at 6; 2 x 1500, 32 over 8: 161,
+// 106, 90, 89, 92).
+constexpr int kSplitItem = 4;
 // Tiles of `tile_rows` rows, `row_per_tok` rows a token; room for `redo` records a tile; split_heads > 0:
 // a plan that may split tiles between blocks, that many key-value heads to a tile.
 AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows, int split_heads,

@@ -8,8 +8,11 @@
 // Where there are few tiles and some are long (drafts or a prompt's last tokens over long pasts),
 // whole tiles would leave most blocks idle or waiting for the longest.  The plan is then split:
 // the tiles' steps of 128 keys are numbered through and every block takes an equal run of them.
-// It is taken where the longest tile exceeds an even share by more than kSplitSlack steps, about
-// what writing and joining the pieces costs.
+// A (tile, key-value head)'s own start and end is counted as kSplitItem steps more: by steps alone the
+// last blocks get many one-step tiles (2048 tokens, 16 heads over 4: 79 us, with it 50).
+// The plan is split where the longest tile exceeds an even share by more than kSplitSlack units, about
+// what writing and joining the pieces costs.  Split against whole at an excess of 101 units 69 against
+// 187 us, 18: 56 / 71, 11: 34 / 46, 10: 50 / 55, 9: 50 / 50, 8: 64 / 60, none: 89 / 74.
 #include "attn_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -20,10 +23,10 @@ __device__ int g_plan_error;
 
 constexpr int kPlanThreads = 1024, kBuckets = 256;
 constexpr int kSplitTiles = kPlanThreads;         // tiles that a split plan may list
-constexpr int kSplitSlack = 6, kSplitMin = 4;     // steps
+constexpr int kSplitSlack = 8, kSplitMin = 4;     // units
 
 // The list of at most kSplitTiles tiles, in a fixed order (a split tile's sums depend on it), with
-// the steps before each tile, and whether to split.  A tile a thread.
+// the units before each tile, and whether to split.  A tile a thread.
 template <typename F>
 __device__ void split_plan(const AttnArgs& a, const AttnPlan& plan, int per, int tile_rows, int grid, F keys_of) {
     __shared__ int s_start[kSplitTiles], s_steps[kSplitTiles], s_warp[kPlanThreads / 32], s_max;
@@ -71,21 +74,21 @@ __device__ void split_plan(const AttnArgs& a, const AttnPlan& plan, int per, int
     s_steps[tid] = t.steps;
     __syncthreads();
     // its place: after the longer tiles, and the equal ones before it
-    int rank = 0, total = 0;
+    int rank = 0;
+    int64_t total = 0;
     for (int j = 0; j < tiles; ++j) {
         const int w = s_steps[j];
         const bool first = w > t.steps || (w == t.steps && j < tid);
         rank += first;
-        t.before += first ? w : 0;
-        total += w;
+        t.before += first ? w + kSplitItem : 0;
+        total += w + kSplitItem;
     }
     if (tid < tiles) plan.tiles[rank] = t;
     if (tid == 0) {
-        const int64_t steps = (int64_t)total * a.HKV;
-        const int share = (int)((steps + grid - 1) / grid);
+        const int64_t units = total * a.HKV, share = (units + grid - 1) / grid;
         int blocks = 0;
-        if (s_max > share + kSplitSlack)
-            blocks = (int)min((int64_t)grid, max(steps / kSplitMin, (int64_t)1));
+        if (s_max + kSplitItem > share + kSplitSlack && total <= INT32_MAX / 2)      // (`before` is 32 bits)
+            blocks = (int)min((int64_t)grid, max(units / kSplitMin, (int64_t)1));
         plan.counts[0] = tiles;
         plan.counts[1] = 0;
         plan.counts[3] = blocks;

@@ -202,23 +202,23 @@ struct ItemSource {
         k = 0;
         at = stop = 0;
         if (shared == 0 || (int)blockIdx.x >= shared) return;
-        // an even share of all steps, tile by tile, key-value head by key-value head
+        // an even share of all units, tile by tile, key-value head by key-value head
         const int lane = threadIdx.x & 31;
         const PlanTile end = plan.tiles[tiles - 1];
-        const int64_t N = (int64_t)(end.before + end.steps) * a.HKV;
+        const int64_t N = (int64_t)(end.before + end.steps + kSplitItem) * a.HKV;
         at = N * blockIdx.x / shared;
         stop = N * (blockIdx.x + 1) / shared;
-        for (int b = 0; b < tiles; b += 32) {          // the tile that holds step `at`
+        for (int b = 0; b < tiles; b += 32) {          // the tile that holds unit `at`
             const bool in = b + lane < tiles && (int64_t)plan.tiles[b + lane].before * a.HKV <= at;
             const unsigned m = __ballot_sync(0xffffffffu, in);
             if (m) k = b + 31 - __clz(m);
         }
         if (lane == 0 && blockIdx.x > 0) {             // for the join
             const PlanTile t = plan.tiles[k];
-            const int h = (int)((at - (int64_t)t.before * a.HKV) / t.steps);
+            const int w = t.steps + kSplitItem, h = (int)((at - (int64_t)t.before * a.HKV) / w);
             // the (tile, head)'s blocks: the first is the last one that begins at or before its
-            // first step (no block is empty: there are at least as many steps as blocks)
-            const int64_t t0 = (int64_t)t.before * a.HKV + (int64_t)h * t.steps;
+            // first step (no share is empty: there are at least as many units as blocks)
+            const int64_t t0 = (int64_t)t.before * a.HKV + (int64_t)h * w + kSplitItem;
             const int c0 = (int)(((t0 + 1) * shared - 1) / N), c1 = (int)(((t0 + t.steps) * shared - 1) / N);
             plan.desc[blockIdx.x] =
                 at > t0 && (int)blockIdx.x == c0 + 1 ? make_int4(k, h, c0, c1) : make_int4(-1, 0, 0, 0);
@@ -239,12 +239,17 @@ struct ItemSource {
                 if (at >= stop) break;
                 const PlanTile t = plan.tiles[k];
                 const int64_t o = at - (int64_t)t.before * a.HKV;
-                const int h = (int)(o / t.steps);
+                const int w = t.steps + kSplitItem, h = (int)(o / w);
                 if (h >= a.HKV) {
                     ++k;
                     continue;
                 }
-                const int s0 = (int)(o - (int64_t)h * t.steps), s1 = (int)min((int64_t)t.steps, s0 + stop - at);
+                const int s0 = (int)(o - (int64_t)h * w) - kSplitItem;
+                if (s0 < 0) {                              // to its first step
+                    at -= s0;
+                    continue;
+                }
+                const int s1 = (int)min((int64_t)t.steps, s0 + stop - at);
                 it = Item{t.n, h, t.q0, t.n_q, t.n_kv, t.index * 2 * tokens, s0, s1,
                           s0 == 0 && s1 == t.steps ? -1 : (int)blockIdx.x * 2 + (s0 == 0 ? 1 : 0)};
                 at += s1 - s0;
@@ -823,7 +828,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a
             float4 y[kBatch][NC];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
-                const int b = min(b0 + k, d.w);                // (past the end: read again, not used)
+                const int b = b0 + k;
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (b > d.w) continue;
                 const int64_t half = ((int64_t)b * 2 + (b == d.z ? 1 : 0)) * kSplitRows + x * kRows;
                 ml[k] = plan.part_ml[half + tr0 + row];
                 const float4* p = reinterpret_cast<const float4*>(plan.part_o) + half * (D / 4) + tr0 + row;
@@ -842,7 +849,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a
 #pragma unroll
             for (int k = 0; k < kBatch; ++k) {
                 // (a piece in which the row sees no key has no sums, whatever lies there)
-                if (b0 + k > d.w || (ml[k].x == -INFINITY && ml[k].y == 0.f)) continue;
+                if (ml[k].x == -INFINITY && ml[k].y == 0.f) continue;
                 const float f = exp2_sfu(ml[k].x - base);
                 l = fmaf(f, ml[k].y, l);
 #pragma unroll
