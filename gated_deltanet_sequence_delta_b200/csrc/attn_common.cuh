@@ -30,6 +30,9 @@ struct AttnArgs {
     void* o;                    // [n_tokens, HQ, D]
     bool bf16;
     void* ws;                   // scratch
+    // paged prompt pieces of at most this many (token, query head of a group) rows go to the kernel that
+    // streams the pages past one m16 product (attn_decode.cu), the others to the tiles; 0: none do
+    int short_rows;
 };
 
 struct AppendArgs {
@@ -54,6 +57,10 @@ struct AppendArgs {
 
 __device__ __forceinline__ SeqRows seq_rows(const AttnArgs& a, int n) {
     return seq_rows(a.cu, a.kv.kv_lens, n, a.T, a.n_tokens, (int64_t)a.kv.max_pages << a.kv.page_shift);
+}
+
+__device__ __forceinline__ bool short_piece(const AttnArgs& a, const SeqRows& r) {
+    return a.short_rows > 0 && r.n_q > 0 && (int64_t)r.n_q * (a.HQ / a.HKV) <= a.short_rows;
 }
 
 // Scratch of the prompt attentions, built by the plan kernel and filled in by the main one.
@@ -85,6 +92,11 @@ constexpr int kSplitRows = 256;
 // (2048 tokens, 16 heads over 4: 79 us at 0, 54 at 2, 49 at 3, 50 at 4, 52 at 6; 2 x 1500, 32 over 8: 161,
 // 106, 90, 89, 92).
 constexpr int kSplitItem = 4;
+// (Rows of a bad table may be listed twice: never past the list's end.)
+__device__ __forceinline__ void list_redo(const AttnPlan& plan, int n, int kvh, int row, int rows) {
+    const int k = atomicAdd(&plan.counts[1], 1);
+    if (k < plan.max_redo) plan.redo[k] = make_int4(n, kvh, row, rows);
+}
 // Tiles of `tile_rows` rows, `row_per_tok` rows a token; room for `redo` records a tile; split_heads > 0:
 // a plan that may split tiles between blocks, that many key-value heads to a tile.
 AttnPlan attn_plan(void* ws, int64_t n_tokens, int n_seqs, int redo, int row_per_tok, int tile_rows, int split_heads,
@@ -133,6 +145,10 @@ __device__ __forceinline__ float gate_out_fast(float o, float z) {
     return o * r;
 }
 
+// Pieces that short_piece() names, against their pages; rows whose result is not finite are listed in
+// the plan.  `ws` as the decode call's.
+constexpr int kShortRows = 16;
+cudaError_t launch_attn_short(const AttnArgs& a, const AttnPlan& plan, void* ws, cudaStream_t s);
 cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
 // bf16 on the tensor cores; the query heads of a group have to fit a tile's rows.

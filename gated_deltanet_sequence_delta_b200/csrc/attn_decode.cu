@@ -1,4 +1,5 @@
-// attn_decode.cu -- one new token per sequence attends to its pages of the key-value cache.
+// attn_decode.cu -- one new token per sequence, or a short piece of them, attends to its pages of the
+// key-value cache.
 //
 //   o_h = sum_j w_j v_j / sum_j w_j,   w_j = e^{scale q_h . k_j - m},  j over the context.
 //
@@ -14,6 +15,17 @@
 // running maximum, sum and unnormalised output in the workspace, two slots a block, and a second
 // small kernel joins them in the order of the blocks (the result does not depend on timing).
 // Lengths live on the device: each block finds its range by a scan over them.
+//
+// An item's start and end count as a few tiles in the split.
+//
+// Measured: 64 ragged contexts to 32K, 8 key-value heads, gated: 550 us for 3.75 GB (6.8 TB/s; 630 us in
+// long runs, where the power limit holds the clock at 1.7 GHz); one context of 262K, 2 heads: 50 us for
+// 268 MB; of 1000: 10 us, the chain of lengths, table, tile and join; fp32, 24 contexts, 64 wide: 71 us
+// for 323 MB.
+//
+// Short pieces (P): the rows are a piece's (token, head) pairs, 16 at most, each with a last key of its
+// own.  Values that only some rows see stay in shared memory; one that is not finite shows in the other
+// rows' outputs, and those rows are listed for the pass that leaves masked places out.
 //
 // Block: a producer warp copies tiles into a ring in shared memory by TMA, 128B-swizzled, one
 // box per page part (rows of a token's head are 128 or 256 bytes, heads and tokens strided);
@@ -60,18 +72,31 @@ struct Cfg {
     static constexpr int kItemCost = 4;
 };
 
+// The context that the kernel reads for a sequence: P, only where the sequence has a short piece.
+template <bool P>
+__device__ __forceinline__ int keys_of(const AttnArgs& a, const SeqRows& r) {
+    return !P || short_piece(a, r) ? r.n_kv : 0;
+}
+template <bool P>
 __device__ __forceinline__ int tiles_of(const AttnArgs& a, int n, int kt, int* bad) {
     const SeqRows r = seq_rows(a, n);
     if (r.bad) *bad = r.bad;
-    return (r.n_kv + kt - 1) / kt;
+    return (keys_of<P>(a, r) + kt - 1) / kt;
+}
+// Where row r of an item is in q, z and o: P, the rows are the piece's (token, query head) pairs.
+template <bool P>
+__device__ __forceinline__ int64_t row_at(const AttnArgs& a, int D, int r) {
+    if constexpr (!P) return (int64_t)r * D;
+    const int G = a.HQ / a.HKV, t = r / G;
+    return ((int64_t)t * a.HQ + (r - t * G)) * D;
 }
 
 // Units of work of sequence n: per head (and row block) its tiles, one unit each, and in front of
 // them the item's cost.  Tile t of an item that begins at unit u is unit u + kItemCost + t; a block
 // has the tiles whose units are in its share.
-template <typename C>
+template <typename C, bool P>
 __device__ __forceinline__ int64_t cost_of(const AttnArgs& a, int n, int subs, int* bad) {
-    const int tiles = tiles_of(a, n, C::KT, bad);
+    const int tiles = tiles_of<P>(a, n, C::KT, bad);
     return tiles > 0 ? (int64_t)(tiles + C::kItemCost) * subs : 0;
 }
 
@@ -160,29 +185,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&x);
 }
 
-template <typename IO, int D, int R>
+template <typename IO, int D, int R, bool P>
 struct Warp;
 
-// bf16: rows are heads, 16 of them; a thread holds rows lane / 4 and lane / 4 + 8.
-template <int D>
-struct Warp<bf16, D, 16> {
+// bf16: rows are heads (P: a piece's (token, head) pairs), 16 of them; a thread holds rows lane / 4 and
+// lane / 4 + 8.
+template <int D, bool P>
+struct Warp<bf16, D, 16, P> {
     using C = Cfg<bf16, D, 16>;
     uint32_t q[D / 16][4];
     float o[D / 8][4];
     float m[2], l[2];
 
-    __device__ __forceinline__ void start(const bf16* qrow, int rows, const float*) {
+    __device__ __forceinline__ void start(const AttnArgs& a, const bf16* qrow, int rows) {
         const int lane = threadIdx.x & 31, r = lane >> 2, c = (lane & 3) * 2;
+        const bf16 *p0 = qrow + row_at<P>(a, D, r) + c, *p1 = qrow + row_at<P>(a, D, r + 8) + c;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            const bf16* p = qrow + k * 16 + c;
-            auto at = [&](int row, int col) {
-                return row < rows ? *reinterpret_cast<const uint32_t*>(p + (int64_t)row * D + col) : 0u;
-            };
-            q[k][0] = at(r, 0);
-            q[k][1] = at(r + 8, 0);
-            q[k][2] = at(r, 8);
-            q[k][3] = at(r + 8, 8);
+            q[k][0] = r < rows ? *reinterpret_cast<const uint32_t*>(p0 + k * 16) : 0u;
+            q[k][1] = r + 8 < rows ? *reinterpret_cast<const uint32_t*>(p1 + k * 16) : 0u;
+            q[k][2] = r < rows ? *reinterpret_cast<const uint32_t*>(p0 + k * 16 + 8) : 0u;
+            q[k][3] = r + 8 < rows ? *reinterpret_cast<const uint32_t*>(p1 + k * 16 + 8) : 0u;
         }
 #pragma unroll
         for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -190,8 +213,10 @@ struct Warp<bf16, D, 16> {
         l[0] = l[1] = 0.f;
     }
 
-    // the warp's KW keys, rows KW w .. of the tile, of which the first `valid` exist (> 0)
-    __device__ __forceinline__ void step(uint8_t* tile, int w, int valid, int, float sc, const float*) {
+    // the warp's KW keys, rows KW w .. of the tile, of which the first `valid` exist (> 0); P: the first
+    // `all` of which every row sees, a row of token t those up to all + t
+    __device__ __forceinline__ void step(const AttnArgs& a, uint8_t* tile, int w, int valid, int all, float sc,
+                                         const float*) {
         constexpr int NS = C::KW / 16;
         const int lane = threadIdx.x & 31;
         uint8_t* vt = tile + C::NB * C::kBlk;
@@ -225,12 +250,20 @@ struct Warp<bf16, D, 16> {
         // the reference m moves only when a score exceeds it by more than 2^8 (weights stay below
         // that), so that a step usually needs no reduction over the row's four threads
         bool grow = false;
+        int sees[2] = {valid, valid};
+        if (P && all < valid) {
+            // (0 * v is not 0 where a value that the row does not see is not finite: that shows in the
+            // output, and the row is done again)
+            const int G = a.HQ / a.HKV;
+            sees[0] = min(valid, all + (lane >> 2) / G);
+            sees[1] = min(valid, all + ((lane >> 2) + 8) / G);
+        }
 #pragma unroll
         for (int j = 0; j < 2 * NS; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int key = j * 8 + (lane & 3) * 2 + (i & 1);
-                s[j][i] = key < valid ? s[j][i] * sc : -INFINITY;
+                s[j][i] = key < sees[i >> 1] ? s[j][i] * sc : -INFINITY;
                 grow = grow || s[j][i] > m[i >> 1] + 8.f;
             }
         if (__any_sync(0xffffffffu, grow)) {
@@ -306,13 +339,13 @@ struct Warp<bf16, D, 16> {
 // more than 2^8 (weights stay below that), so that a step usually needs no reduction over the
 // warp; l is a lane's own sum over its keys until the end.
 template <int D, int R>
-struct Warp<float, D, R> {
+struct Warp<float, D, R, false> {
     using C = Cfg<float, D, R>;
     static constexpr int E = D / 32, NS = C::KW / 8;
     float o[R][E];
     float m[R], l[R];
 
-    __device__ __forceinline__ void start(const float*, int, const float*) {
+    __device__ __forceinline__ void start(const AttnArgs&, const float*, int) {
 #pragma unroll
         for (int r = 0; r < R; ++r) {
             m[r] = -INFINITY;
@@ -322,7 +355,8 @@ struct Warp<float, D, R> {
         }
     }
 
-    __device__ __forceinline__ void step(uint8_t* tile, int w, int valid, int rows, float sc, const float* sq) {
+    __device__ __forceinline__ void step(const AttnArgs&, uint8_t* tile, int w, int valid, int, float sc,
+                                         const float* sq) {
         const int lane = threadIdx.x & 31, key = lane >> 2, part = lane & 3;
         const uint8_t* vt = tile + C::NB * C::kBlk;
         float s[NS][R];
@@ -422,21 +456,23 @@ struct Warp<float, D, R> {
 // Where a block is in its share: sequence, (head, row block) of it, tile of that item, the tile's
 // unit.
 struct Cursor {
-    int n, sub, tile, tiles, len;
+    int n, sub, tile, tiles, len, q0, n_q;
     int64_t unit;
 };
-template <typename C>
+template <typename C, bool P>
 __device__ __forceinline__ void cursor_load(const AttnArgs& a, Cursor& c) {
     while (true) {      // (the last sequence ends the search, tiles or not)
         const SeqRows r = seq_rows(a, c.n);
-        c.len = r.n_kv;
-        c.tiles = (r.n_kv + C::KT - 1) / C::KT;
+        c.len = keys_of<P>(a, r);
+        c.tiles = (c.len + C::KT - 1) / C::KT;
+        c.q0 = r.q0;
+        c.n_q = r.n_q;
         if (c.tiles > 0 || c.n + 1 >= a.n_seqs) return;
         ++c.n;
     }
 }
 // To the next tile; false if it is not in the block's share, which ends before unit `end`.
-template <typename C>
+template <typename C, bool P>
 __device__ __forceinline__ bool cursor_next(const AttnArgs& a, Cursor& c, int subs, int64_t end) {
     ++c.unit;
     if (++c.tile < c.tiles) return c.unit < end;
@@ -446,22 +482,23 @@ __device__ __forceinline__ bool cursor_next(const AttnArgs& a, Cursor& c, int su
     if (++c.sub == subs) {
         c.sub = 0;
         if (++c.n >= a.n_seqs) return false;
-        cursor_load<C>(a, c);
+        cursor_load<C, P>(a, c);
     }
     return true;
 }
 
-template <typename IO, int D, int R>
+// P: short pieces of prompts instead of one token per sequence (bf16, one row block: hb = 1).
+template <typename IO, int D, int R, bool P>
 __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_constant__ CUtensorMap tk,
                                                                   const __grid_constant__ CUtensorMap tv, AttnArgs a,
-                                                                  int hb) {
+                                                                  int hb, AttnPlan plan) {
     using C = Cfg<IO, D, R>;
     constexpr int S = C::kStages;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t s_warp[kThreads / 32];
     __shared__ Place s_place;
     __shared__ __align__(8) uint64_t full[S], empty[S];
-    __shared__ int s_dead;
+    __shared__ int s_dead, s_redo;
     // ring tiles 1024-byte aligned (the swizzle's period)
     uint8_t* ring = smem_raw + ((1024 - (tc::smem_u32(smem_raw) & 1023)) & 1023);
     float* merge = reinterpret_cast<float*>(ring + S * C::kStage);
@@ -475,24 +512,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
             tc::mbar_init(&empty[i], C::TW);
         }
         tc::fence_mbar_init();
-        s_dead = 0;
+        s_dead = s_redo = 0;
     }
     tc::grid_dependency_sync();
     int bad = 0;
     const Place pl = find_place(
-        a.n_seqs, [&](int n) { return cost_of<C>(a, n, subs, &bad); }, blockIdx.x, gridDim.x, s_warp, &s_place);
+        a.n_seqs, [&](int n) { return cost_of<C, P>(a, n, subs, &bad); }, blockIdx.x, gridDim.x, s_warp, &s_place);
     if (bad && blockIdx.x == 0) atomicMax(&g_decode_attn_error, bad);
     // contexts of no keys: zeros, a sequence's rows by one block
     for (int n = blockIdx.x; n < a.n_seqs; n += gridDim.x) {
         const SeqRows r = seq_rows(a, n);
-        if (!r.bad && r.n_kv == 0)
-            for (int i = tid; i < a.HQ * D; i += kThreads) store_elem((IO*)a.o, (int64_t)n * a.HQ * D + i, 0.f);
+        if (!r.bad && r.n_kv == 0 && (!P || short_piece(a, r)))
+            for (int i = tid; i < r.n_q * a.HQ * D; i += kThreads)
+                store_elem((IO*)a.o, (int64_t)r.q0 * a.HQ * D + i, 0.f);
     }
     const Partials part = partials(a.ws, R, D);
     if (tid == 0) {      // for the join
         int4 d = make_int4(-1, 0, 0, 0);
         if (pl.n >= 0) {
-            const int tiles = tiles_of(a, pl.n, C::KT, &bad);
+            const int tiles = tiles_of<P>(a, pl.n, C::KT, &bad);
             const int sub = (int)((pl.at - pl.before) / (tiles + C::kItemCost));
             // unit of the item's first tile, and the blocks that hold its tiles: unit u is in the
             // last block that begins at or before it
@@ -508,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
     const int64_t end = pl.total * (blockIdx.x + 1) / pl.blocks;
     Cursor cur;
     cur.n = pl.n;
-    cursor_load<C>(a, cur);
+    cursor_load<C, P>(a, cur);
     {
         const int64_t in_seq = pl.at - pl.before;
         cur.sub = (int)(in_seq / (cur.tiles + C::kItemCost));
@@ -561,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 tc::tma_load_3d(tile + (lk * C::NB + lb) * C::kBlk + lg * rows_box * 128, lk ? &tv : &tk, &full[st],
                                 lb * (128 / (int)sizeof(IO)), kvh, (int)row);
             }
-            more = cursor_next<C>(a, cur, subs, end);
+            more = cursor_next<C, P>(a, cur, subs, end);
         }
         if (!ok) {      // an expired wait: let every copy that was issued land before leaving
             if (lane == 0) atomicMax(&g_decode_attn_error, GDN_DEVERR_TIMEOUT);
@@ -572,13 +610,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
 
     // ---- consumers
     const int team = warp / C::TW, w = warp % C::TW;
-    Warp<IO, D, R> st;
+    Warp<IO, D, R, P> st;
     const float sc = a.scale * kLog2e;
     bool ok = true, fresh = true, from_start = false, more = true;
     for (int it = 0; more; ++it) {
         const int kvh = cur.sub / hb, h0 = kvh * G + (cur.sub - kvh * hb) * R;
-        const int rows = min(R, (kvh + 1) * G - h0);
-        const int64_t qrow = ((int64_t)cur.n * a.HQ + h0) * D;
+        const int rows = P ? cur.n_q * G : min(R, (kvh + 1) * G - h0);
+        const int64_t qrow = ((int64_t)cur.q0 * a.HQ + h0) * D;
         if (fresh) {
             from_start = cur.tile == 0;
             if constexpr (sizeof(IO) == 4) {
@@ -587,19 +625,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                     sq[i] = i < rows * D ? ((const float*)a.q)[qrow + i] : 0.f;
                 tc::named_bar(1, kConsumers);
             }
-            st.start((const IO*)a.q + qrow, rows, sq);
+            st.start(a, (const IO*)a.q + qrow, rows);
             fresh = false;
         }
         if (it % C::Teams == team) {
             const int s = it % S;
             if (ok) ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[s], (uint32_t)((it / S) & 1)));
-            const int valid = min(C::KW, cur.len - cur.tile * C::KT - w * C::KW);
-            if (ok && valid > 0) st.step(ring + s * C::kStage, w, valid, rows, sc, sq);
+            const int left = cur.len - cur.tile * C::KT - w * C::KW, valid = min(C::KW, left);
+            if (ok && valid > 0) st.step(a, ring + s * C::kStage, w, valid, left - cur.n_q + 1, sc, sq);
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&empty[s]);
         }
         const bool item_end = cur.tile + 1 == cur.tiles;
-        more = cursor_next<C>(a, cur, subs, end);
+        const int n = cur.n, past = cur.len - cur.n_q;
+        more = cursor_next<C, P>(a, cur, subs, end);
         if (item_end || !more) {
             // the segment is over: join the eight warps
             if (!ok && lane == 0) s_dead = 1;
@@ -628,12 +667,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                     }
                 }
                 if (whole) {
+                    const bool none = P && past < 0 && past + r / G < 0;             // the row sees no key
                     const float inv = 1.0f / l;
                     const float y[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+                    const int64_t at = qrow + row_at<P>(a, D, r) + c;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int64_t at = qrow + (int64_t)r * D + c + e;
-                        store_elem((IO*)a.o, at, a.z ? gate_out(y[e], load_elem((const IO*)a.z, at)) : y[e]);
+                        float out = none ? 0.f : y[e];
+                        if constexpr (P)
+                            if (!(fabsf(out) <= 3.4028235e38f)) s_redo = 1;
+                        if (a.z && !none) out = gate_out(out, load_elem((const IO*)a.z, at + e));
+                        store_elem((IO*)a.o, at + e, out);
                     }
                 } else {
                     *reinterpret_cast<float4*>(part.o + (slot * R + r) * D + c) = x;
@@ -641,38 +685,51 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 }
             }
             tc::named_bar(1, kConsumers);
+            if constexpr (P)
+                if (tid == 0 && s_redo) {
+                    list_redo(plan, n, kvh, 0, rows);
+                    s_redo = 0;          // (set again only after the next item's first barrier)
+                }
             fresh = true;
         }
     }
     if (s_dead && tid == 0) atomicMax(&g_decode_attn_error, GDN_DEVERR_TIMEOUT);
 }
 
-// Joins the pieces of the items that more than one block took.  Block (c - 1, r): row r of the item
-// that block c of the first kernel left to it.  A warp takes every eighth piece, kBatch of them in
-// flight.
+// Joins the pieces of the items that more than one block took: of the item that block c of the first
+// kernel left to it.  Many pieces (a long context over many blocks): block (c - 1, r) is row r, a warp
+// takes every eighth piece.  At most kBatch: block (c - 1, y) is rows 8 y .. 8 y + 7, a warp each, and
+// the other y have nothing to do (16 rows of 512 items: 4 against 12 us).  All of a warp's loads
+// are in flight at once, kBatch at a time.
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32, kBatch = 8;
 template <int E> struct Vec;
 template <> struct Vec<2> { using T = float2; };
 template <> struct Vec<4> { using T = float4; };
-template <typename IO, int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
+template <typename IO, int D, int R, bool P>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, AttnPlan plan) {
     constexpr int E = D / 32;
     __shared__ float s_o[kJoinWarps][D];
     __shared__ float s_m[kJoinWarps], s_l[kJoinWarps];
     tc::grid_dependency_sync();
     const Partials part = partials(a.ws, R, D);
     const int4 d = part.desc[blockIdx.x + 1];
-    const int first = d.x, last = d.y, r = blockIdx.y, G = a.HQ / a.HKV;
-    if (first < 0 || d.w % G + r >= G) return;
+    const int first = d.x, last = d.y, G = a.HQ / a.HKV;
+    if (first < 0) return;
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const bool few = last - first < kBatch;
+    const int r = few ? blockIdx.y * kJoinWarps + w : blockIdx.y;
+    if (few && blockIdx.y * kJoinWarps >= R) return;
+    const SeqRows sr = P ? seq_rows(a, d.z) : SeqRows{d.z, 1, 0, 0};
+    if (P ? r >= sr.n_q * G : (r >= R || d.w % G + r >= G)) return;          // (a warp, or the block)
+    const int start = few ? first : first + w, stride = few ? 1 : kJoinWarps;
     auto slot = [&](int b) { return ((int64_t)b * 2 + (b == first ? 1 : 0)) * R + r; };
     float m = -INFINITY, l = 0.f, x[E] = {};
-    for (int b0 = first + w; b0 <= last; b0 += kBatch * kJoinWarps) {
+    for (int b0 = start; b0 <= last; b0 += kBatch * stride) {
         float2 ml[kBatch];
         typename Vec<E>::T y[kBatch];
 #pragma unroll
         for (int i = 0; i < kBatch; ++i) {
-            const int b = min(b0 + i * kJoinWarps, last);          // (past the end: read again, not used)
+            const int b = min(b0 + i * stride, last);          // (past the end: read again, not used)
             ml[i] = part.ml[slot(b)];
             y[i] = reinterpret_cast<const typename Vec<E>::T*>(part.o + slot(b) * D)[lane];
         }
@@ -686,13 +743,28 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
         for (int e = 0; e < E; ++e) x[e] *= g;
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
-            if (b0 + i * kJoinWarps <= last) {
+            if (b0 + i * stride <= last) {
                 const float f = exp2f(ml[i].x - base);
                 const float* v = reinterpret_cast<const float*>(&y[i]);
                 l = fmaf(f, ml[i].y, l);
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] = fmaf(f, v[e], x[e]);
             }
+    }
+    const bool none = P && sr.n_kv - sr.n_q + r / G < 0;         // the row sees no key
+    const int64_t at = ((int64_t)sr.q0 * a.HQ + d.w) * D + row_at<P>(a, D, r);
+    // column c of the row; whether it is finite
+    auto put = [&](int c, float y) {
+        if (none) y = 0.f;
+        store_elem((IO*)a.o, at + c, a.z && !none ? gate_out(y, load_elem((const IO*)a.z, at + c)) : y);
+        return fabsf(y) <= 3.4028235e38f;
+    };
+    bool finite = true;
+    if (few) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) finite = put(lane * E + e, x[e] / l) && finite;
+        if (P && !__all_sync(0xffffffffu, finite) && lane == 0) list_redo(plan, d.z, d.w / G, r, 1);
+        return;
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_o[w][lane * E + e] = x[e];
@@ -713,17 +785,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
             y = fmaf(f, s_o[i][tid], y);
             sum = fmaf(f, s_l[i], sum);
         }
-        y /= sum;
-        const int64_t at = ((int64_t)d.z * a.HQ + d.w + r) * D + tid;
-        store_elem((IO*)a.o, at, a.z ? gate_out(y, load_elem((const IO*)a.z, at)) : y);
+        finite = put(tid, y / sum);
     }
+    if constexpr (P)
+        if (__syncthreads_or(!finite) && tid == 0) list_redo(plan, d.z, d.w / G, r, 1);
 }
 
-template <typename IO, int D, int R>
-cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+template <typename IO, int D, int R, bool P = false>
+cudaError_t launch(const AttnArgs& a, cudaStream_t s, const AttnPlan& plan = AttnPlan{}) {
     using C = Cfg<IO, D, R>;
     static_assert(C::kStages >= 4 && C::kSmem <= 226 * 1024, "decode: shared memory");
-    const int G = a.HQ / a.HKV, hb = (G + R - 1) / R;
+    const int G = a.HQ / a.HKV, hb = (G + R - 1) / R;          // (P: 1)
     int dev = 0, sms = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -746,14 +818,15 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         !make_map(&tv, dt, a.kv.v, 3, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B, l2))
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    e = allow_smem((const void*)attn_decode_kernel<IO, D, R>, C::kSmem, done);
+    e = allow_smem((const void*)attn_decode_kernel<IO, D, R, P>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_decode_kernel<IO, D, R>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tk, tv, a, hb);
+    e = launch_pdl(attn_decode_kernel<IO, D, R, P>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tk, tv, a, hb, plan);
     if (e != cudaSuccess) return e;
     count_launch();
     if (grid == 1) return cudaSuccess;           // nothing to join
-    e = launch_pdl(attn_join_kernel<IO, D, R>, dim3((unsigned)(grid - 1), (unsigned)(G < R ? G : R)), dim3(kJoinThreads), 0,
-                   s, a);
+    const int64_t rows = P ? a.n_tokens * G : G;              // the most that an item can have
+    e = launch_pdl(attn_join_kernel<IO, D, R, P>, dim3((unsigned)(grid - 1), (unsigned)(rows < R ? rows : R)),
+                   dim3(kJoinThreads), 0, s, a, plan);
     if (e == cudaSuccess) count_launch();
     return e;
 }
@@ -777,6 +850,12 @@ size_t attn_decode_bytes(int D) {
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
     if (a.bf16) return a.D == 128 ? launch<bf16, 128, 16>(a, s) : launch<bf16, 64, 16>(a, s);
     return a.D == 128 ? launch_f32<128>(a, s) : launch_f32<64>(a, s);
+}
+
+cudaError_t launch_attn_short(const AttnArgs& args, const AttnPlan& plan, void* ws, cudaStream_t s) {
+    AttnArgs a = args;
+    a.ws = ws;
+    return a.D == 128 ? launch<bf16, 128, kShortRows, true>(a, s, plan) : launch<bf16, 64, kShortRows, true>(a, s, plan);
 }
 
 cudaError_t read_attn_decode_error(int32_t* out) {

@@ -36,7 +36,7 @@ __device__ void split_plan(const AttnArgs& a, const AttnPlan& plan, int per, int
     if (tid < a.n_seqs) {
         const SeqRows r = seq_rows(a, tid);
         if (r.bad) atomicMax(&g_plan_error, r.bad);
-        mine = (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
+        mine = short_piece(a, r) ? 0 : (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
     }
     int incl = mine;
 #pragma unroll
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Att
     for (int pass = 0; pass < 2; ++pass) {
         for (int n = tid >> 5; n < a.n_seqs; n += kPlanThreads / 32) {
             const SeqRows r = seq_rows(a, n);
-            const int tiles = (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
+            const int tiles = short_piece(a, r) ? 0 : (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
             for (int t = lane; t < tiles; t += 32) {
                 const int keys = keys_of(r, t);
                 const int at = atomicAdd(&s_count[kBuckets - 1 - min(keys / width, kBuckets - 1)], 1);

@@ -186,12 +186,6 @@ struct Item {
     __device__ __forceinline__ int first(int tokens) const { return steps(0, tokens) > 0 ? 0 : 1; }
 };
 
-// (Rows of a bad table may be listed twice: never past the list's end.)
-__device__ __forceinline__ void list_redo(const AttnPlan& plan, int n, int kvh, int row, int rows) {
-    const int k = atomicAdd(&plan.counts[1], 1);
-    if (k < plan.max_redo) plan.redo[k] = make_int4(n, kvh, row, rows);
-}
-
 // The items of this block, in order.  Warp-wide.
 struct ItemSource {
     int tiles, shared, k;
@@ -899,18 +893,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a
     if (redo && tid == 0) list_redo(plan, t.n, h, tok0 * G + tr0, min(kJoinRows, tokens * G - tr0));
 }
 
+// The workspace: the plan's, then what the kernel for short pieces wants.
+AttnPlan plan_of(void* ws, int64_t n_tokens, int n_seqs, int HQ, int HKV, int D) {
+    return attn_plan(ws, n_tokens, n_seqs, 16 * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
+}
+size_t short_at(const AttnPlan& plan) { return (plan.bytes + 255) / 256 * 256; }
+
 template <int D>
-cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_tiles(const AttnArgs& a, const AttnPlan& plan, int blocks, cudaStream_t s) {
     using C = Cfg<D>;
     const int G = a.HQ / a.HKV, tokens = kRows / G;
-    const AttnPlan plan = attn_plan(a.ws, a.n_tokens, a.n_seqs, 16 * a.HKV, 1, 2 * tokens, a.HKV, D);
-    int dev = 0, sms = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e != cudaSuccess) return e;
-    const int blocks = sms < kSplitGrid ? sms : kSplitGrid;
-    e = launch_attn_plan(a, plan, 1, 2 * tokens, blocks, s);
-    if (e != cudaSuccess) return e;
+    cudaError_t e;
     CUtensorMap tq, tk, tv, tz, to;
     const int page = 1 << a.kv.page_shift;
     const int box_rows = a.kv.table && page < kKeys ? page : kKeys;
@@ -946,7 +939,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         count_launch();
     }
-    return launch_attn_redo(a, plan, s);
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -954,11 +947,33 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s) {
 bool attn_tc_supported(int HQ, int HKV) { return HQ / HKV <= kRows; }
 
 size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D) {
-    const AttnPlan p = attn_plan(nullptr, n_tokens, n_seqs, 16 * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
-    return p.bytes;
+    return short_at(plan_of(nullptr, n_tokens, n_seqs, HQ, HKV, D)) + attn_decode_bytes(D);
 }
 
-cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s) { return a.D == 128 ? launch<128>(a, s) : launch<64>(a, s); }
+cudaError_t launch_attn_tc(const AttnArgs& args, cudaStream_t s) {
+    AttnArgs a = args;
+    const int G = a.HQ / a.HKV;
+    const AttnPlan plan = plan_of(a.ws, a.n_tokens, a.n_seqs, a.HQ, a.HKV, a.D);
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const int blocks = sms < kSplitGrid ? sms : kSplitGrid;
+    // Pieces of a few rows (drafts, single tokens) leave most of a tile's rows idle and pay its chain of
+    // products and softmax per step, so they are streamed instead.  Lengths are on the device: here it
+    // is decided by the mean, since two passes one after the other lose where few pieces are short.
+    // Streamed against tiles at a mean of 16 rows: 80 against 102 us (64 x 4 tokens, 32 heads over 8, past
+    // 1000), 65 / 69 (8 x 4, 16 over 4, 16000); 4: 67 / 83 (64 x 1, 2000); 32: 42 / 35 (16 x 8); 35, one
+    // piece of 512 and 63 tokens: 100 / 96.
+    if (a.kv.table && a.n_tokens * G <= (int64_t)kShortRows * a.n_seqs) a.short_rows = kShortRows;
+    const bool all_short = a.short_rows > 0 && a.n_tokens * G <= kShortRows;
+    e = launch_attn_plan(a, plan, 1, 2 * (kRows / G), blocks, s);
+    if (e == cudaSuccess && !all_short)
+        e = a.D == 128 ? launch_tiles<128>(a, plan, blocks, s) : launch_tiles<64>(a, plan, blocks, s);
+    if (e == cudaSuccess && a.short_rows > 0)
+        e = launch_attn_short(a, plan, static_cast<uint8_t*>(a.ws) + short_at(plan), s);
+    return e == cudaSuccess ? launch_attn_redo(a, plan, s) : e;
+}
 
 cudaError_t read_attn_tc_error(int32_t* out) {
     cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_tc_error, sizeof(int32_t));

@@ -404,6 +404,100 @@ def test_slots_past_the_contexts_cost_nothing(new, past, page):
         assert torch.isfinite(o).all() and ws[4:8].view(torch.int32).item() == 0
 
 
+# Short pieces: at most 16 (token, head) rows a sequence on average; some longer ones among them.
+SHORT = [
+    # D, HQ, HKV, page, new, past, gate
+    (128, 8, 2, 16, [4] * 5, [0, 100, 2500, 63, 17], True),
+    (128, 4, 4, 64, [1, 16, 3], [300, 9000, 0], False),
+    (64, 8, 2, 32, [1] * 12 + [20], [5, 0, 64, 700, 127, 128, 129, 1, 2, 3, 4, 3000, 900], True),
+    (64, 6, 2, 128, [5, 0, 2, 6, 4], [1000, 50, 0, 31, 12000], False),          # 15 and 18 rows
+    (128, 16, 1, 16, [1, 1, 0, 1], [4000, 0, 10, 129], True),
+    (128, 16, 2, 64, [1] * 9 + [9], [77, 0, 500, 31, 32, 33, 2000, 63, 64, 400], False),
+    (128, 4, 2, 16, [3, 2, 7, 4, 8], [-3, -1, -7, 60, -3], True),                # rows before the context
+    (128, 1, 1, 16, [16, 17, 1, 3], [250, 1000, 0, 6000], False),
+]
+
+
+@pytest.mark.parametrize("D,HQ,HKV,page,new,past,gate", SHORT)
+def test_short_pieces(D, HQ, HKV, page, new, past, gate):
+    torch, G = _torch()
+    assert sum(new) * (HQ // HKV) <= 16 * len(new)
+    g = _gen(61)
+    c = Cache([max(n + p, 0) for n, p in zip(new, past)], HKV, D, page, "bf16", 62)
+    cu = _cu(new)
+    q = _draw(g, (cu[-1], HQ, D), "bf16", 1.5)
+    z = _draw(g, (cu[-1], HQ, D), "bf16") if gate else None
+    ws = torch.zeros(G.attn_prefill_workspace_bytes(cu[-1], len(new), HQ, HKV, D, 1), dtype=torch.uint8, device="cuda")
+    call = lambda: G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, _i32(cu), z=z, workspace=ws)
+    o = call()
+    assert ws[4:8].view(torch.int32).item() == 0                       # no row done again
+    for i, n in enumerate(new):
+        if n == 0:
+            continue
+        kn, vn = c.seq(i) if c.totals[i] else (np.zeros((0, HKV, D)),) * 2
+        r = slice(cu[i], cu[i + 1])
+        _check_rows(o[r], q[r], kn, vn, c.totals[i] - n, D ** -0.5, "bf16", None if z is None else z[r], f"seq {i}")
+    assert torch.equal(o, call())                                      # bit for bit
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("past", [37, 9000])
+def test_short_pieces_nonfinite_in_masked_places(bad, past):
+    """A value (or key) that only the later tokens of a piece see leaves the earlier ones alone, in a
+    piece that one block holds and in one that many share."""
+    torch, G = _torch()
+    D, HQ, HKV, n = 128, 8, 2, 4
+    g = _gen(63)
+    for in_v in (True, False):
+        c = Cache([past + n, past + n], HKV, D, 16, "bf16", 64)
+        q = _draw(g, (2 * n, HQ, D), "bf16", 1.5)
+        cu = _i32([0, n, 2 * n])
+        clean = G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cu)
+        pos = past + 2                                                 # tokens 2 and 3 of the piece see it
+        page = c.table[1, pos // 16].item()
+        (c.v if in_v else c.k)[page, pos % 16, 1, 5] = bad
+        o = G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cu)
+        assert torch.equal(o[:n], clean[:n])                           # another sequence
+        assert torch.equal(o[n:, :4], clean[n:, :4])                   # the other key-value head
+        kn, vn = c.seq(1)
+        m = past + 2
+        _check_rows(o[n:n + 2, 4:], q[n:n + 2, 4:], kn[:m, 1:], vn[:m, 1:], past, D ** -0.5, "bf16", None, "rows before")
+        if in_v:
+            assert not torch.isfinite(o[n + 2:, 4:, 5]).any()
+        assert G.gdn_attn_status() == 0
+
+
+def test_short_pieces_agree_with_decode():
+    """Single tokens through the piece call are what the decode call returns, up to their roundings:
+    each lies within the bound of the definition."""
+    torch, G = _torch()
+    r = np.random.default_rng(9)
+    ctx = r.integers(1, 90, 700).tolist()
+    ctx[300] = 5000
+    c = Cache(ctx, 2, 64, 16, "bf16", 65)
+    q = _draw(_gen(66), (len(ctx), 8, 64), "bf16", 1.5)
+    o = G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, _i32(list(range(len(ctx) + 1))))
+    _check_decode(c, q, o, "bf16", None, 64 ** -0.5)
+    _check_decode(c, q, G.gdn_attn_decode(q, c.k, c.v, c.table, c.lens), "bf16", None, 64 ** -0.5)
+    assert G.gdn_attn_status() == 0
+
+
+def test_short_pieces_back_to_back():
+    """Launches over one workspace, without a synchronisation between them, repeat bit for bit."""
+    torch, G = _torch()
+    new = [4] * 9 + [12]
+    c = Cache([n + p for n, p in zip(new, [3000, 10, 777, 64, 1500, 0, 9000, 5, 128, 2000])], 4, 128, 16, "bf16", 67)
+    cu = _i32(_cu(new))
+    q = _draw(_gen(68), (sum(new), 12, 128), "bf16")
+    ws = torch.empty(G.attn_prefill_workspace_bytes(sum(new), len(new), 12, 4, 128, 1), dtype=torch.uint8, device="cuda")
+    outs = [torch.empty_like(q) for _ in range(2)]
+    for i in range(600):
+        G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cu, o=outs[i > 0], workspace=ws)
+    assert torch.equal(*outs)
+    assert G.gdn_attn_status() == 0
+
+
 # ---- decode -----------------------------------------------------------------------------
 DECODE = [
     # dtype, D, HQ, HKV, page, contexts, gate
