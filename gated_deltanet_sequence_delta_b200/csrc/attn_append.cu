@@ -11,6 +11,9 @@
 // forms their rotary/2 sines and cosines once (the heads share them) in shared memory and then
 // walks (token, head, pair of 16-byte chunks) units.  A unit holds both halves of its pairs, so
 // every access is 16 bytes wide and in-place rotation of q is safe.
+//
+// Measured: 37K tokens of 32 + 2 x 8 heads of 128, bf16, from the fused projection: 162.5 us for 908 MB
+// (5.6 TB/s, 0.87 of a copy); 64 tokens: 3.4 us, one chain of loads.
 #include "attn_common.cuh"
 
 namespace gdn {
@@ -174,7 +177,9 @@ cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s) {
     const int n = a.bf16 ? 8 : 4;
     const int units = ((a.q ? a.HQ : 0) + 2 * a.HKV) * (a.D / (2 * n));     // per token
     // Few tokens: one per block and its units over several blocks, one unit a thread, since the
-    // call's time is then the latency of one chain of loads.  Many: kMaxTok tokens share a block.
+    // call's time is then the latency of one chain of loads.  Many: kMaxTok tokens share a block and
+    // their sines.  Few against many, bf16, 16 + 2 x 4 heads of 128: 3.3 / 6.7 us at 64 tokens, 6.7 / 7.0
+    // at 1024, 10.2 / 8.7 at 2048, 17.9 / 12.3 at 4096.
     const bool few = a.n_tokens < 1024;
     const int tok = few ? 1 : kMaxTok;
     const int ub = few ? (units + kThreads - 1) / kThreads : 1;

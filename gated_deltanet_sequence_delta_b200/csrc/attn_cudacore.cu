@@ -8,7 +8,9 @@
 // The rows of a tile are (token, query head of the group) pairs of one key-value head, so the
 // group shares each key and value that is staged.  64 rows x 64 keys a step, 256 threads, a
 // 4 x 4 block of scores and 4 x D/16 outputs each; row statistics stay within a half-warp.
-// Bound: shared-memory reads (8 16-byte reads per 64 FMAs), about half of the fp32 rate.
+// Bound: shared-memory reads (8 16-byte reads per 64 FMAs): 0.71 of their rate, half of the fp32 one.
+// Measured, fp32: 37.2 TFLOP/s for 8000 tokens (16 heads over 4 of 128), 22 (171 us) for 3 x 1111 (8 over
+// 2 of 64), where the longest tiles' chain of steps ends last.
 //
 // Masked places never enter a sum, neither their scores nor 0 * v_j, so infinities and NaN in
 // values a row does not see leave it alone.

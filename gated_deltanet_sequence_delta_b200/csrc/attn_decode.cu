@@ -820,7 +820,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t s, const AttnPlan& plan = Att
     static std::atomic<uint64_t> done{0};
     e = allow_smem((const void*)attn_decode_kernel<IO, D, R, P>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(attn_decode_kernel<IO, D, R, P>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tk, tv, a, hb, plan);
+    e = launch_pdl(attn_decode_kernel<IO, D, R, P>, dim3((unsigned)grid), dim3(kThreads), C::kSmem, s, tk, tv, a, hb,
+                   plan);
     if (e != cudaSuccess) return e;
     count_launch();
     if (grid == 1) return cudaSuccess;           // nothing to join
@@ -855,7 +856,8 @@ cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s) {
 cudaError_t launch_attn_short(const AttnArgs& args, const AttnPlan& plan, void* ws, cudaStream_t s) {
     AttnArgs a = args;
     a.ws = ws;
-    return a.D == 128 ? launch<bf16, 128, kShortRows, true>(a, s, plan) : launch<bf16, 64, kShortRows, true>(a, s, plan);
+    return a.D == 128 ? launch<bf16, 128, kShortRows, true>(a, s, plan)
+                      : launch<bf16, 64, kShortRows, true>(a, s, plan);
 }
 
 cudaError_t read_attn_decode_error(int32_t* out) {

@@ -35,6 +35,11 @@
 // 2^8, and the accumulated O rescaled in tensor memory: a row's first steps.  The weights are rounded
 // to bf16 for the product (half a step, 2^-8 relative, each); their sum is taken before the rounding.
 //
+// Measured, bf16: one prompt of 32K tokens, 16 heads over 4 of 128: 3.4 ms in short runs (1.28 PFLOP/s,
+// 0.76 of the matrix rate), 3.9-4.05 ms in long ones, where the power limit holds the clock at 1.6 GHz
+// (0.78 of the sustained matrix rate); 75K packed tokens, gated: 3.6-3.8 ms, 3.9-4.15 in long runs; pieces
+// over contexts to 24K, gated: 1.6 ms (1.8); 18 to 40 tokens over 13K in pages of 16: 92 us.
+//
 // Masked weights are exact zeros, but 0 * v is not 0 where v is infinite or NaN.  Values past
 // the last key that any row of the block sees are cleared in shared memory; a value inside the
 // diagonal that is not finite shows in the outputs, whose tile is then put on a list that the
