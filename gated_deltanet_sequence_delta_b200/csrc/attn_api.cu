@@ -61,6 +61,7 @@ bool any_overlap(std::initializer_list<Range> outs, std::initializer_list<Range>
 
 // What the three attention calls have in common once their sizes are checked.
 gdn_status check_attn(const AttnArgs& a, gdn_dtype io, size_t need, void* workspace, size_t workspace_bytes) {
+    if (a.kv.table && a.kv.n_pages == 0) return GDN_ERR_SHAPE;
     if (!workspace || workspace_bytes < need) return GDN_ERR_WORKSPACE;
     if (!a.q || !a.kv.k || !a.kv.v || !a.o) return GDN_ERR_NULL;
     if (!all_aligned({a.q, a.kv.k, a.kv.v, a.kv.table, a.kv.kv_lens, a.cu, a.z, a.o, workspace})) return GDN_ERR_ALIGN;

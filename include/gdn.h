@@ -495,7 +495,8 @@ GDN_API gdn_status gdn_decode_status(int32_t* device_error);
  * enter its sums, whatever they hold (infinities, NaN).
  *
  * Shared by the four calls:
- *   k_cache, v_cache [n_pages, page_size, HKV, D] io_dtype; page_size 16, 32, 64 or 128
+ *   k_cache, v_cache [n_pages, page_size, HKV, D] io_dtype; page_size 16, 32, 64 or 128;
+ *               the calls that read the cache want one page at least
  *   block_table [n_seqs, max_pages] int32: page block_table[n][p / page_size] holds position p
  *               of sequence n at offset p % page_size.  Entries past a sequence's context are
  *               not read.  Sequences may share pages that a call only reads.

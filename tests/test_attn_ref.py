@@ -210,6 +210,11 @@ def test_paged_refusals(L, call):
     assert call(L, o=A + 16 * MB) == 5 and call(L, ws=A + 101 * MB) == 5 and call(L, o=A + 100 * MB) == 5
 
 
+@pytest.mark.parametrize("call", [_paged_call, _decode])
+def test_a_cache_without_pages_is_refused(L, call):
+    assert call(L, n_pages=0) == 2 and call(L, n_pages=-1) == 2
+
+
 def test_paged_nothing_to_do_and_status(L):
     assert _paged_call(L, cu=None) == 1
     assert _paged_call(L, T=0) == 0 and _paged_call(L, N=0) == 0 and _decode(L, B=0) == 0 and _decode(L, B=-1) == 2
