@@ -82,7 +82,7 @@ size_t prefill_bytes(int64_t n_tokens, int32_t n_seqs, int32_t HQ, int32_t HKV, 
     // the kernels count tiles (of one token or more, per key-value head) in 32 bits
     if ((n_tokens + n_seqs) * (int64_t)HQ > INT32_MAX) return 0;
     if (io == GDN_BF16 && gdn::attn_tc_supported(HQ, HKV)) return gdn::attn_tc_bytes(n_tokens, n_seqs, HQ, HKV, D);
-    return gdn::attn_cudacore_bytes(n_tokens, n_seqs, HQ, HKV);
+    return gdn::attn_cudacore_bytes(n_tokens, n_seqs, HQ, HKV, D);
 }
 
 // A prompt call whose sizes are checked.

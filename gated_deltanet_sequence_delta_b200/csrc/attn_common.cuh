@@ -159,7 +159,7 @@ cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
 cudaError_t launch_attn_redo(const AttnArgs& a, const AttnPlan& p, cudaStream_t s);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_decode_bytes(int D);
-size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV);
+size_t attn_cudacore_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D);
 
 // Read (and clear) the device word each file's kernels set on a bad table or an expired wait.
 cudaError_t read_append_error(int32_t* out);

@@ -404,6 +404,52 @@ def test_slots_past_the_contexts_cost_nothing(new, past, page):
         assert torch.isfinite(o).all() and ws[4:8].view(torch.int32).item() == 0
 
 
+# Prompts on the CUDA cores whose tiles several blocks share: few tiles (up to four pieces, from three
+# steps of 64 keys on), and more (two or three, from six steps on); bf16 takes them for wide groups.
+SHARED = [
+    # dtype, D, HQ, HKV, lens, gate
+    ("fp32", 64, 4, 2, [129], True),
+    ("fp32", 128, 4, 1, [700], False),
+    ("fp32", 64, 8, 2, [256, 193, 128, 1], True),
+    ("fp32", 128, 2, 2, [65, 0, 450], False),
+    ("fp32", 64, 8, 8, [500, 400, 330], True),
+    ("fp32", 64, 8, 2, [900, 320, 321, 384, 500, 37], False),
+    ("bf16", 64, 130, 1, [200], True),
+]
+
+
+@pytest.mark.parametrize("dtype,D,HQ,HKV,lens,gate", SHARED)
+def test_prefill_shared_tiles(dtype, D, HQ, HKV, lens, gate):
+    torch, G = _torch()
+    g = _gen(71)
+    cu = _cu(lens)
+    q = _draw(g, (1, cu[-1], HQ, D), dtype, 1.5)
+    k, v = (_draw(g, (1, cu[-1], HKV, D), dtype) for _ in range(2))
+    z = _draw(g, q.shape, dtype) if gate else None
+    call = lambda: G.gdn_attn_prefill(q, k, v, cu_seqlens=_i32(cu), z=z)
+    o = call()
+    for i, n in enumerate(lens):
+        r = slice(cu[i], cu[i + 1])
+        rows = sorted({j for j in (0, 1, 63, 64, 65, 127, 128, 191, 192, 193, n // 2, n - 2, n - 1) if 0 <= j < n})
+        _check_rows(o[0, r], q[0, r], _np(k[0, r]), _np(v[0, r]), 0, D ** -0.5, dtype,
+                    None if z is None else z[0, r], f"seq {i}", rows)
+    assert torch.equal(o, call())                                      # bit for bit
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_shared_tiles_nonfinite_in_masked_places(bad):
+    """A key and a value late in the past leave the tokens before them alone, in a shared tile too."""
+    torch, G = _torch()
+    q, k, v = (_draw(_gen(72 + i), (1, 400, 2, 64), "fp32") for i in range(3))
+    clean = G.gdn_attn_prefill(q, k, v)
+    k[0, 301, 0, 3], v[0, 301, 0, 7] = bad, bad
+    o = G.gdn_attn_prefill(q, k, v)
+    assert torch.equal(o[:, :301], clean[:, :301]) and torch.equal(o[:, :, 1], clean[:, :, 1])
+    assert not torch.isfinite(o[0, 399, 0, 7])
+    assert G.gdn_attn_status() == 0
+
+
 # Short pieces: at most 16 (token, head) rows a sequence on average; some longer ones among them.
 SHORT = [
     # D, HQ, HKV, page, new, past, gate
