@@ -404,6 +404,32 @@ def test_slots_past_the_contexts_cost_nothing(new, past, page):
         assert torch.isfinite(o).all() and ws[4:8].view(torch.int32).item() == 0
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("count,past0,page", [(400, 0, 16), (6, 5000, 64)])
+def test_slots_past_the_contexts_where_both_tiles_end(D, count, past0, page):
+    """Pieces of 64 tokens whose two tiles of 32 end in one step of 128 keys, as whole tiles and as tiles
+    that blocks share: neither tile's product sees the slots behind the context (NaN here) before they
+    are cleared, so no row is done again and every call gives the same bits."""
+    torch, G = _torch()
+    g = _gen(26)
+    past = [past0 + 128 * (i % 3) + 13 * i % 64 for i in range(count)]
+    assert all((p + 31) // 128 == (p + 63) // 128 for p in past)
+    c = Cache([64 + p for p in past], 2, D, page, "bf16", 27)
+    cu = _cu([64] * count)
+    q = _draw(g, (cu[-1], 8, D), "bf16")
+    ws = torch.zeros(G.attn_prefill_workspace_bytes(cu[-1], count, 8, 2, D, 1), dtype=torch.uint8, device="cuda")
+    call = lambda o: G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, _i32(cu), o=o, workspace=ws)
+    first, o = call(torch.empty_like(q)), torch.empty_like(q)
+    for _ in range(50):
+        call(o)
+        assert ws[4:8].view(torch.int32).item() == 0 and torch.equal(o, first)
+    for i in (0, 1, count - 1):
+        kn, vn = c.seq(i)
+        _check_rows(o[64 * i:64 * i + 64], q[64 * i:64 * i + 64], kn, vn, past[i], D ** -0.5, "bf16", None,
+                    f"sequence {i}", [0, 31, 32, 63])
+    assert G.gdn_attn_status() == 0
+
+
 # Prompts on the CUDA cores whose tiles several blocks share: few tiles (up to four pieces, from three
 # steps of 64 keys on), and more (two or three, from six steps on); bf16 takes them for wide groups.
 SHARED = [
