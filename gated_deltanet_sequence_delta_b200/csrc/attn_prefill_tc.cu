@@ -41,10 +41,10 @@
 // over contexts to 24K, gated: 1.6 ms (1.8); 18 to 40 tokens over 13K in pages of 16: 92 us.
 //
 // Masked weights are exact zeros, but 0 * v is not 0 where v is infinite or NaN.  Values past
-// the last key that any row of the block sees are cleared in shared memory, by one tile for both
-// and before either tile's product reads them; a value inside the diagonal that is not finite shows
-// in the outputs, whose tile is then put on a list that the CUDA-core kernel, which leaves masked
-// places out of its sums, does again.
+// the last key that any row of the block sees are cleared in shared memory, by each tile before its
+// product reads them; a value inside the diagonal that is not finite shows in the outputs, whose
+// tile is then put on a list that the CUDA-core kernel, which leaves masked places out of its sums,
+// does again.
 #include "attn_common.cuh"
 #include "tc_ptx.cuh"
 
@@ -280,8 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
     // product has read them; v_last: the item's last values are there
     __shared__ __align__(8) uint64_t s_full[2], turn[2], p_full[2], pv_done[2], v_last[2];
     __shared__ __align__(8) uint64_t kv_full[S], kv_empty[S], item_full[kItems], item_empty[kItems], drain[2];
-    // cleared: what lies behind the item's last value is zeros (one barrier an item of the ring)
-    __shared__ __align__(8) uint64_t cleared[kItems];
     __shared__ Item s_item[kItems];
     __shared__ uint32_t s_tmem;
     __shared__ int s_timeout;
@@ -310,7 +308,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(&item_full[i], 1);
             tc::mbar_init(&item_empty[i], 11);
-            tc::mbar_init(&cleared[i], 4);
         }
         tc::mbar_init(&drain[0], 1);
         tc::mbar_init(&drain[1], 1);
@@ -397,10 +394,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         if (i + 1 == total && ok && lane == 0) tc::mbar_arrive(&v_last[x]);
                         __syncwarp();
                         wait(&p_full[x], mine + i);
-                        // Tile A clears the last values of both.  (The barrier passes to the item kItems
-                        // later once both tiles' softmax warps are done with this one, so its phase cannot
-                        // be missed.)
-                        if (x == 1 && i + 1 == total && it.steps(0, tokens) == total) wait(&cleared[r % kItems], r / kItems);
                         tc::tc_fence_after();
                         if (ok && tc::elect_one()) {
                             const uint64_t v_off = (uint64_t)((t % S) * (C::kTile >> 4));
@@ -563,10 +556,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
             // counted from the item's first step
             const int first_key = it.s0 * kKeys;
             const int lim = tok < it.ntok(x, tokens) ? it.past() + it.tok + x * tokens + tok - first_key : INT32_MAX;
-            // the tile that clears the values past the item's last key, in the item's last step (A, where
-            // it takes that step): the first such key, or 0
-            const int clear_from = x == ((x == 0 ? steps : other) == total ? 0 : 1)
-                                       ? max(it.end(0, tokens), it.end(1, tokens)) - first_key : 0;
+            // The first of the values past the item's last key, for a tile that takes the last step.  Each
+            // tile clears them for its own product, which waits for its own weights only: the second one's
+            // zeros meet zeros, and are over before its product gives the values' place back.  (Clearing
+            // once, with a barrier between the tiles, costs 1 to 4 percent of a long prompt's time.)
+            const int clear_from = steps == total ? max(it.end(0, tokens), it.end(1, tokens)) - first_key : INT32_MAX;
             float m = -INFINITY, l = 0.f;
             bool finite = true;
             for (int i = 0; i < steps; ++i) {
@@ -599,24 +593,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                     if (i > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&pv_done[x], (uint32_t)(done + i - 1) & 1u));
                     tc::tc_fence_after();
                 };
-                if (i + 1 == total && clear_from > 0) {
+                if (clear_from - j0 < kKeys) {
+                    // Values that no row of the block sees may be anything: clear them, every warp its
+                    // share, whatever rows it has.  (The MMA warp, which sees every copy land in turn,
+                    // tells when they are there.)
+                    const int slot = (t0 + 2 * total - 1) % S;                // the item's last values
+                    ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&v_last[x], (uint32_t)lasts & 1u));
+                    if (!ok) break;
+                    uint8_t* v = ring + slot * C::kTile;
                     const int first = clear_from - j0;
-                    if (first < kKeys) {
-                        // Values that no row of the block sees may be anything: clear them, every warp its
-                        // share, whatever rows it has.  (The MMA warp, which sees every copy land in turn,
-                        // tells when they are there.)
-                        const int slot = (t0 + 2 * total - 1) % S;            // the item's last values
-                        ok = __all_sync(0xffffffffu, tc::mbar_wait_short(&v_last[x], (uint32_t)lasts & 1u));
-                        if (!ok) break;
-                        uint8_t* v = ring + slot * C::kTile;
-                        for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
-                            const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
-                            *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-                        }
-                        tc::fence_async_smem();
+                    for (int e = row; e < (kKeys - first) * 8 * C::kHalves; e += 128) {
+                        const int vr = first + e / (8 * C::kHalves), c = e % (8 * C::kHalves);
+                        *reinterpret_cast<uint4*>(v + (c >> 3) * C::kHalf + vr * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
                     }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(&cleared[r % kItems]);
+                    tc::fence_async_smem();
                 }
                 bool stand = false;
                 if (!masked) {
