@@ -33,11 +33,14 @@ gdn_status check_heads(gdn_dtype io, int32_t HQ, int32_t HKV, int32_t D) {
     return GDN_OK;
 }
 
-// The cache: row numbers (page * page_size + offset) stay within 32 bits.
+// Positions and tokens are 32-bit in the kernels, which look up to two steps of 128 past the last one.
+constexpr int64_t kMaxPositions = (int64_t)INT32_MAX - 255;
+
+// The cache: row numbers (page * page_size + offset) stay within 32 bits, positions below the limit.
 gdn_status check_pages(int32_t n_pages, int32_t page_size, int32_t max_pages) {
     if (n_pages < 0 || page_size <= 0 || max_pages < 0) return GDN_ERR_SHAPE;
     if (page_shift_of(page_size) < 0) return GDN_ERR_UNSUPPORTED;
-    if ((int64_t)n_pages * page_size > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX)
+    if ((int64_t)n_pages * page_size > INT32_MAX || (int64_t)max_pages * page_size > kMaxPositions)
         return GDN_ERR_UNSUPPORTED;
     return GDN_OK;
 }
@@ -78,7 +81,7 @@ gdn_status check_attn(const AttnArgs& a, gdn_dtype io, size_t need, void* worksp
 }
 
 size_t prefill_bytes(int64_t n_tokens, int32_t n_seqs, int32_t HQ, int32_t HKV, int32_t D, gdn_dtype io) {
-    if (n_tokens < 0 || n_tokens > INT32_MAX || n_seqs < 0 || check_heads(io, HQ, HKV, D) != GDN_OK) return 0;
+    if (n_tokens < 0 || n_tokens > kMaxPositions || n_seqs < 0 || check_heads(io, HQ, HKV, D) != GDN_OK) return 0;
     // the kernels count tiles (of one token or more, per key-value head) in 32 bits
     if ((n_tokens + n_seqs) * (int64_t)HQ > INT32_MAX) return 0;
     if (io == GDN_BF16 && gdn::attn_tc_supported(HQ, HKV)) return gdn::attn_tc_bytes(n_tokens, n_seqs, HQ, HKV, D);

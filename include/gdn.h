@@ -506,7 +506,8 @@ GDN_API gdn_status gdn_decode_status(int32_t* device_error);
  *               not appended and sees no key.
  *   cu_seqlens  [n_seqs + 1] int32: new tokens cu_seqlens[n] .. cu_seqlens[n + 1] - 1 belong to
  *               sequence n.  Rows from cu_seqlens[n_seqs] on are left as they were.
- *   D 64 or 128, HQ % HKV == 0, at most 1024 heads.
+ *   D 64 or 128, HQ % HKV == 0, at most 1024 heads; n_pages * page_size below 2^31, max_pages *
+ *   page_size (and the prompt calls' tokens) at most 2^31 - 256.
  * The tables are checked on the device, where they live: a sequence whose cu_seqlens or kv_lens
  * entries are out of range is skipped (its outputs are left as they were), a page number out of
  * range is never followed (what would have been written there is dropped; a sequence that reads

@@ -215,6 +215,23 @@ def test_a_cache_without_pages_is_refused(L, call):
     assert call(L, n_pages=0) == 2 and call(L, n_pages=-1) == 2
 
 
+@pytest.mark.parametrize("call", [_paged_call, _decode])
+def test_table_rows_near_the_end_of_32_bits(L, call):
+    """The kernels' look past a context's last position stays within 32 bits: a table row may hold 2^31 - 256
+    positions (the call then gets as far as its workspace), and no more."""
+    most = 2 ** 31 - 256
+    for page in (16, 128):
+        assert call(L, page=page, width=most // page, ws=None) == 6
+        assert call(L, page=page, width=most // page + 1) == 4
+    assert _append(L, width=most // 16 + 1) == 4
+
+
+def test_tokens_near_the_end_of_32_bits(L):
+    size = lambda n: L.gdn_attn_prefill_workspace_bytes(n, 1, 1, 1, 64, 1)
+    assert size(2 ** 31 - 256) > 0 and size(2 ** 31 - 255) == 0
+    assert _prefill(L, B=1, N=1, T=2 ** 31 - 255, HQ=1, HKV=1) == 4
+
+
 def test_paged_nothing_to_do_and_status(L):
     assert _paged_call(L, cu=None) == 1
     assert _paged_call(L, T=0) == 0 and _paged_call(L, N=0) == 0 and _decode(L, B=0) == 0 and _decode(L, B=-1) == 2
