@@ -25,6 +25,13 @@ constexpr int kPlanThreads = 1024, kBuckets = 256;
 constexpr int kSplitTiles = kPlanThreads;         // tiles that a split plan may list
 constexpr int kSplitSlack = 8, kSplitMin = 4;     // units
 
+// Tiles of a sequence in the list.  The sequences of a proper table have plan.max_tiles together at most.
+// Those of a decreasing cu_seqlens may name rows over and over, in sum more than 32 bits count: a list that
+// would be longer than its place is not made.
+__device__ __forceinline__ int64_t tiles_of(const AttnArgs& a, const SeqRows& r, int per, int tile_rows) {
+    return short_piece(a, r) ? 0 : ((int64_t)r.n_q * per + tile_rows - 1) / tile_rows;
+}
+
 // The list of at most kSplitTiles tiles, in a fixed order (a split tile's sums depend on it), with
 // the units before each tile, and whether to split.  A tile a thread.
 template <typename F>
@@ -36,7 +43,7 @@ __device__ void split_plan(const AttnArgs& a, const AttnPlan& plan, int per, int
     if (tid < a.n_seqs) {
         const SeqRows r = seq_rows(a, tid);
         if (r.bad) atomicMax(&g_plan_error, r.bad);
-        mine = short_piece(a, r) ? 0 : (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
+        mine = (int)tiles_of(a, r, per, tile_rows);      // (within the 1024 that can_split allows, and so the sum)
     }
     int incl = mine;
 #pragma unroll
@@ -52,7 +59,7 @@ __device__ void split_plan(const AttnArgs& a, const AttnPlan& plan, int per, int
         if (i < (tid >> 5)) base += s_warp[i];
         tiles += s_warp[i];
     }
-    tiles = min(tiles, plan.max_tiles);      // (sequences of a bad table may overlap)
+    if (tiles > plan.max_tiles) tiles = 0;
     s_start[tid] = base + incl - mine;
     __syncthreads();
     // this thread's tile: the last sequence that starts at or before it and has tiles
@@ -99,9 +106,13 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Att
                                                                  int grid) {
     __shared__ int s_count[kBuckets];
     __shared__ int s_max;
+    __shared__ unsigned long long s_tiles;
     const int tid = threadIdx.x, lane = tid & 31;
     for (int i = tid; i < kBuckets; i += kPlanThreads) s_count[i] = 0;
-    if (tid == 0) s_max = 1;
+    if (tid == 0) {
+        s_max = 1;
+        s_tiles = 0;
+    }
     __syncthreads();
     tc::grid_dependency_sync();
     auto keys_of = [&](const SeqRows& r, int t) {          // keys that the tile's last row sees
@@ -113,23 +124,31 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(AttnArgs a, Att
         return;
     }
     int mx = 1;
+    int64_t all = 0;
     for (int n = tid; n < a.n_seqs; n += kPlanThreads) {
         const SeqRows r = seq_rows(a, n);
         if (r.bad) atomicMax(&g_plan_error, r.bad);
         mx = max(mx, r.n_kv);
+        all += tiles_of(a, r, per, tile_rows);
     }
+    for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+    if (lane == 0) atomicAdd(&s_tiles, (unsigned long long)all);
     atomicMax(&s_max, mx);
     __syncthreads();
+    if (s_tiles > (unsigned long long)plan.max_tiles) {
+        if (tid == 0) plan.counts[0] = plan.counts[1] = plan.counts[3] = 0;
+        return;
+    }
     const int width = (s_max - 1) / kBuckets + 1;
     // a sequence per warp, a tile per lane
     for (int pass = 0; pass < 2; ++pass) {
         for (int n = tid >> 5; n < a.n_seqs; n += kPlanThreads / 32) {
             const SeqRows r = seq_rows(a, n);
-            const int tiles = short_piece(a, r) ? 0 : (int)(((int64_t)r.n_q * per + tile_rows - 1) / tile_rows);
+            const int tiles = (int)tiles_of(a, r, per, tile_rows);
             for (int t = lane; t < tiles; t += 32) {
                 const int keys = keys_of(r, t);
                 const int at = atomicAdd(&s_count[kBuckets - 1 - min(keys / width, kBuckets - 1)], 1);
-                // sequences of a bad table may overlap: never past the list's end
+                // (tables that change under the call: never past the list's end)
                 if (pass == 1 && at < plan.max_tiles)
                     plan.tiles[at] = PlanTile{n, t, r.q0, r.n_q, r.n_kv, max((keys + 127) / 128, 1), 0, 0};
             }

@@ -511,8 +511,10 @@ GDN_API gdn_status gdn_decode_status(int32_t* device_error);
  * The tables are checked on the device, where they live: a sequence whose cu_seqlens or kv_lens
  * entries are out of range is skipped (its outputs are left as they were), a page number out of
  * range is never followed (what would have been written there is dropped; a sequence that reads
- * it gets undefined outputs); other sequences are not affected.  The first such finding is kept
- * in a device word that gdn_attn_status reads.
+ * it gets undefined outputs); other sequences are not affected, but for those that a decreasing
+ * cu_seqlens gives the same rows: their outputs are undefined, and where such sequences name more
+ * rows in all than there are, a prompt call may write none.  The first such finding is kept in a
+ * device word that gdn_attn_status reads.
  */
 
 /*

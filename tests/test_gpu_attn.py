@@ -821,6 +821,24 @@ def test_bad_tables_are_reported_and_stay_contained(dtype):
     assert torch.equal(kc.view(-1, 256)[s], c.k.view(-1, 256)[s])
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("count", [9, 199])
+def test_sequences_that_name_the_same_rows_over_and_over(dtype, count):
+    """A cu_seqlens that goes up and down gives many sequences all rows: more tiles than the plan has room for,
+    however few or many.  None is listed, and the next call over the workspace is as ever."""
+    torch, G = _torch()
+    g = _gen(43)
+    T, H = 1000, 8
+    q, k, v = (_draw(g, (1, T, H, 64), dtype) for _ in range(3))
+    ws = torch.empty(G.attn_prefill_workspace_bytes(T, count, H, H, 64, int(dtype == "bf16")), dtype=torch.uint8, device="cuda")
+    o = torch.full_like(q, 7.0)
+    G.gdn_attn_prefill(q, k, v, cu_seqlens=_i32([T * (i & 1) for i in range(count + 1)]), o=o, workspace=ws)
+    assert G.gdn_attn_status() == 1 and (o == 7.0).all()
+    G.gdn_attn_prefill(q, k, v, cu_seqlens=_i32([0] * count + [T]), o=o, workspace=ws)
+    _check_rows(o[0], q[0], _np(k[0]), _np(v[0]), 0, 0.125, dtype, None, "one sequence", [0, 500, T - 1])
+    assert G.gdn_attn_status() == 0
+
+
 # ---- as they are used -----------------------------------------------------------------
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_a_prompt_in_pieces_then_tokens_equals_the_whole(dtype):
