@@ -153,6 +153,7 @@ cudaError_t launch_attn_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_cudacore(const AttnArgs& a, cudaStream_t s);
 // bf16 on the tensor cores; the query heads of a group have to fit a tile's rows.
 bool attn_tc_supported(int HQ, int HKV);
+// 0: more sequences than the lists count.
 size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D);
 cudaError_t launch_attn_tc(const AttnArgs& a, cudaStream_t s);
 // Redo the rows that the plan lists, on CUDA cores.

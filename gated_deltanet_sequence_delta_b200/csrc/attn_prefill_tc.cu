@@ -902,8 +902,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_rows_kernel(AttnArgs a
 }
 
 // The workspace: the plan's, then what the kernel for short pieces wants.
+constexpr int kRedoPerHead = kSplitRows / kJoinRows;      // records of a (tile, key-value head), at most: the join's
 AttnPlan plan_of(void* ws, int64_t n_tokens, int n_seqs, int HQ, int HKV, int D) {
-    return attn_plan(ws, n_tokens, n_seqs, 16 * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
+    return attn_plan(ws, n_tokens, n_seqs, kRedoPerHead * HKV, 1, 2 * (kRows / (HQ / HKV)), HKV, D);
 }
 size_t short_at(const AttnPlan& plan) { return (plan.bytes + 255) / 256 * 256; }
 
@@ -955,7 +956,10 @@ cudaError_t launch_tiles(const AttnArgs& a, const AttnPlan& plan, int blocks, cu
 bool attn_tc_supported(int HQ, int HKV) { return HQ / HKV <= kRows; }
 
 size_t attn_tc_bytes(int64_t n_tokens, int n_seqs, int HQ, int HKV, int D) {
-    return short_at(plan_of(nullptr, n_tokens, n_seqs, HQ, HKV, D)) + attn_decode_bytes(D);
+    const AttnPlan plan = plan_of(nullptr, n_tokens, n_seqs, HQ, HKV, D);
+    // the list of rows to do again is counted in 32 bits (many millions of sequences pass that)
+    if ((int64_t)plan.max_tiles * kRedoPerHead * HKV > INT32_MAX) return 0;
+    return short_at(plan) + attn_decode_bytes(D);
 }
 
 cudaError_t launch_attn_tc(const AttnArgs& args, cudaStream_t s) {

@@ -232,6 +232,13 @@ def test_tokens_near_the_end_of_32_bits(L):
     assert _prefill(L, B=1, N=1, T=2 ** 31 - 255, HQ=1, HKV=1) == 4
 
 
+def test_sequences_past_what_the_lists_count(L):
+    """Rows to do again are listed in records counted in 32 bits, 16 a key-value head and tile."""
+    size = lambda n: L.gdn_attn_prefill_workspace_bytes(1, n, 8, 8, 64, 1)
+    assert size(2 ** 24 - 2) > 0 and size(2 ** 24 - 1) == 0 and size(2 ** 27) == 0
+    assert _paged_call(L, T=1, N=2 ** 24 - 1, HQ=8, HKV=8, D=64) == 4
+
+
 def test_paged_nothing_to_do_and_status(L):
     assert _paged_call(L, cu=None) == 1
     assert _paged_call(L, T=0) == 0 and _paged_call(L, N=0) == 0 and _decode(L, B=0) == 0 and _decode(L, B=-1) == 2
