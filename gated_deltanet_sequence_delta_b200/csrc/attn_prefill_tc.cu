@@ -83,9 +83,10 @@ struct Cfg {
     __device__ static constexpr int o_col(int x) { return 512 - 2 * D + x * D; }
 };
 
-// 2^x for two floats, |x| < 126 or x < 0 (below 2^-126 it stays there): x = n + f, n the nearest
-// integer by the magic-number addition, 2^f on [-1/2, 1/2] by the cubic of least relative error
-// (7.5e-5, found by the Remez exchange), n added to the exponent field.
+// 2^x for two floats, x taken as -126 below it and as 127 above it: x = n + f, n the nearest integer
+// by the magic-number addition, 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, found
+// by the Remez exchange), n added to the exponent field, which has room for it between the bounds.
+// (A weight of 2^127, whatever it stands for, makes the row's sum exceed kGrowSum: the step is done again.)
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -105,7 +106,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 __device__ __forceinline__ void exp2_poly(float& a, float& b) {
-    const uint64_t x = pack2(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+    const uint64_t x = pack2(fminf(fmaxf(a, -126.0f), 127.0f), fminf(fmaxf(b, -126.0f), 127.0f));
     const uint64_t magic = pack2(12582912.0f, 12582912.0f);
     const uint64_t t = add2(x, magic);
     const uint64_t n = add2(t, pack2(-12582912.0f, -12582912.0f));

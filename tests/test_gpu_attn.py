@@ -264,6 +264,70 @@ def test_prefill_growing_and_sharp_scores(dtype):
     _check_rows(o[0], q[0], _np(k[0]).copy()[::-1], _np(v[0]), 0, 128 ** -0.5, dtype, None, "falling", _some(T, 2))
 
 
+def test_prefill_narrow_heads_growing_and_sharp_scores():
+    """The same at the other head width, whose steps form a share of the weights in another way."""
+    torch, G = _torch()
+    g = _gen(13)
+    T = 700
+    q, k, v = _draw(g, (1, T, 2, 64), "bf16"), _draw(g, (1, T, 1, 64), "bf16"), _draw(g, (1, T, 1, 64), "bf16")
+    up = (torch.linspace(0.02, 6.0, T, device="cuda") ** 2)[None, :, None, None]
+    k = (k * up).to(k.dtype)
+    o = G.gdn_attn_prefill(q, k, v)
+    _check_rows(o[0], q[0], _np(k[0]), _np(v[0]), 0, 0.125, "bf16", None, "growing", _some(T, 1))
+    o = G.gdn_attn_prefill(q, k.flip(1).contiguous(), v)
+    _check_rows(o[0], q[0], _np(k[0]).copy()[::-1], _np(v[0]), 0, 0.125, "bf16", None, "falling", _some(T, 2))
+
+
+JUMPS = [20, 100, 126, 127, 128, 129, 130, 150, 160, 200, 250, 260, 300, 390, 450, 511, 520, 2000]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_one_key_far_above_the_others(D):
+    """One key whose score is `jump` (in powers of two of its weight) above all others, in a step that the
+    rows see whole and after one that has set their reference, at every place modulo 16."""
+    torch, G = _torch()
+    g = _gen(18)
+    T, cases = 384, [(j, p) for j in JUMPS for p in range(16)]
+    q = torch.full((1, T * len(cases), 1, D), 8.0, dtype=torch.bfloat16, device="cuda")
+    k, v = torch.zeros_like(q), _draw(g, q.shape, "bf16")
+    for i, (jump, place) in enumerate(cases):           # scale q . k = k, with q = 8 and scale 1 / (8 D)
+        k[0, i * T + 128 + 48 + place] = jump * np.log(2.0)
+    o = G.gdn_attn_prefill(q, k, v, cu_seqlens=_i32(_cu([T] * len(cases))), scale=1 / (8 * D))
+    for i, (jump, place) in enumerate(cases):
+        s = slice(i * T, i * T + T)
+        _check_rows(o[0, s], q[0, s], _np(k[0, s]), _np(v[0, s]), 0, 1 / (8 * D), "bf16", None,
+                    f"jump {jump} at {place}", [150, 256, 383])
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_paged_one_key_far_above_the_others(D):
+    """The same where blocks share a tile's steps: in two steps one after the other, so that one of them is
+    not the first of its block's."""
+    torch, G = _torch()
+    new, total = 20, 2000
+    c = Cache([total], 1, D, 16, "bf16", 19)
+    q = torch.full((new, 1, D), 8.0, dtype=torch.bfloat16, device="cuda")
+    at = c.slots(0, 0, total)
+    for jump in JUMPS:
+        for place in (3, 14, 15):
+            c.k.view(-1, 1, D)[at] = 0.0
+            c.k.view(-1, 1, D)[at[[5 * 128 + 32 + place, 6 * 128 + 64 + place]]] = jump * np.log(2.0)
+            o = G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, _i32([0, new]), scale=1 / (8 * D))
+            kn, vn = c.seq(0)
+            _check_rows(o, q, kn, vn, total - new, 1 / (8 * D), "bf16", None, f"jump {jump} at {place}", [0, 19])
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+def test_prefill_narrow_heads_other_scales(scale):
+    torch, G = _torch()
+    g = _gen(14)
+    q, k, v = _draw(g, (1, 300, 2, 64), "bf16"), _draw(g, (1, 300, 2, 64), "bf16"), _draw(g, (1, 300, 2, 64), "bf16")
+    o = G.gdn_attn_prefill(q, k, v, scale=scale)
+    _check_rows(o[0], q[0], _np(k[0]), _np(v[0]), 0, scale, "bf16", None, f"scale {scale}", _some(300, 1, 8))
+
+
 @pytest.mark.parametrize("scale", [0.0, -0.3])
 def test_prefill_other_scales(scale):
     torch, G = _torch()
