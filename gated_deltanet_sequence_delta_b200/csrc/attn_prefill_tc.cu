@@ -5,8 +5,7 @@
 // in one pass over the keys with a running reference m per row.  FLOPs: 4 D per (row, key) pair,
 // 2 D x 2 products; bound by the tensor cores and, at D = 64, by the exponentials: an SM takes
 // 16 of them a clock in its special-function units, so the 128 x 128 weights of a step cost 1024
-// clocks there against 1024 (D = 128) or 512 (D = 64) of the two products.  A share of them is
-// therefore formed on the FMA pipes (exp2_poly).
+// clocks there against 1024 (D = 128) or 512 (D = 64) of the two products.
 //
 // Rows.  A tile is 128 rows, the (token, query head of the group) pairs of one key-value head:
 // 128 / G tokens by G heads, so that the group shares every key and value that is staged and
@@ -73,20 +72,13 @@ struct Cfg {
     static constexpr int kRing = D == 128 ? 5 : 8;               // key / value tiles
     static constexpr int kSmem = (2 + kRing) * kTile + 1024;
     static constexpr bool kOneS = D == 128;                      // one S for both tiles
-    // An eighth of the exponentials on the FMA pipes pays where they bound the step (D = 64: 242
-    // against 255 us for 8K tokens, 16 heads over 4); at D = 128 it costs (3.48 against 3.43 ms for
-    // 32K tokens).
-    static constexpr bool kPoly = D == 64;
     // TMEM columns
     __device__ static constexpr int s_col(int x) { return kOneS ? 0 : x * 128; }
     __device__ static constexpr int p_col(int x) { return (kOneS ? 128 : 256) + x * 64; }
     __device__ static constexpr int o_col(int x) { return 512 - 2 * D + x * D; }
 };
 
-// 2^x for two floats, x taken as -126 below it and as 127 above it: x = n + f, n the nearest integer
-// by the magic-number addition, 2^f on [-1/2, 1/2] by the cubic of least relative error (7.5e-5, found
-// by the Remez exchange), n added to the exponent field, which has room for it between the bounds.
-// (A weight of 2^127, whatever it stands for, makes the row's sum exceed kGrowSum: the step is done again.)
+// Two floats side by side, and the FMA pipes' two-wide operations on them.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
@@ -105,22 +97,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ void exp2_poly(float& a, float& b) {
-    const uint64_t x = pack2(fminf(fmaxf(a, -126.0f), 127.0f), fminf(fmaxf(b, -126.0f), 127.0f));
-    const uint64_t magic = pack2(12582912.0f, 12582912.0f);
-    const uint64_t t = add2(x, magic);
-    const uint64_t n = add2(t, pack2(-12582912.0f, -12582912.0f));
-    const uint64_t f = fma2(n, pack2(-1.0f, -1.0f), x);
-    uint64_t p = fma2(f, pack2(0.05517166852951050f, 0.05517166852951050f),
-                      pack2(0.2426111251115799f, 0.2426111251115799f));
-    p = fma2(p, f, pack2(0.6932609677314758f, 0.6932609677314758f));
-    p = fma2(p, f, pack2(0.9999280571937561f, 0.9999280571937561f));
-    float pa, pb, ta, tb;
-    unpack2(p, pa, pb);
-    unpack2(t, ta, tb);
-    a = __int_as_float(__float_as_int(pa) + (__float_as_int(ta) << 23));
-    b = __int_as_float(__float_as_int(pb) + (__float_as_int(tb) << 23));
-}
 __device__ __forceinline__ float exp2_sfu(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -138,9 +114,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 // A row's weights 2^(s sc - base) as bf16 in tensor memory (keys 2j, 2j + 1 in column j); returns
-// their sum.  `free` is called before the first write.  MASKED: keys past `last` weigh exactly 0,
-// and all the others go through the special-function units (the cubic does not reach 0).
-template <bool MASKED, bool POLY, typename F>
+// their sum.  `free` is called before the first write.  MASKED: keys past `last` weigh exactly 0.
+// All weights go through the special-function units, which keep NaN and infinities: forming an eighth
+// of them on the FMA pipes by a cubic (2^f on [-1/2, 1/2], the integer part added to the exponent, the
+// argument bound on both sides) takes as long or longer: 227 against 224 us for 8K tokens, 16 heads over 4
+// of 64, 2.94 / 2.86 ms for 32K; of 128, 3.48 / 3.43 ms.
+template <bool MASKED, typename F>
 __device__ __forceinline__ float weights(const float (&s)[128], float sc, float base, int last, uint32_t tp, F free) {
     const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
     uint64_t sum[4] = {0, 0, 0, 0};
@@ -154,8 +133,6 @@ __device__ __forceinline__ float weights(const float (&s)[128], float sc, float 
             if (MASKED) {
                 e0 = c + j > last ? 0.f : exp2_sfu(e0);
                 e1 = c + j + 1 > last ? 0.f : exp2_sfu(e1);
-            } else if (POLY && (j & 15) == 14) {
-                exp2_poly(e0, e1);
             } else {
                 e0 = exp2_sfu(e0);
                 e1 = exp2_sfu(e1);
@@ -611,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 }
                 bool stand = false;
                 if (!masked) {
-                    const float sum = weights<false, C::kPoly>(s, sc, m, 0, tp, free);
+                    const float sum = weights<false>(s, sc, m, 0, tp, free);
                     stand = !__any_sync(0xffffffffu, !(sum <= kGrowSum) && lim != INT32_MAX);
                     if (stand) l += sum;
                 }
@@ -659,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                         }
                     }
                     const float base = m == -INFINITY ? 0.f : m;
-                    l += weights<true, false>(s, sc, base, lim - j0, tp, free);
+                    l += weights<true>(s, sc, base, lim - j0, tp, free);
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();

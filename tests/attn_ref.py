@@ -7,8 +7,8 @@ kernels' result o differs from the exact one by at most
     A * (r_P + 2 e_s + (n + 16) u) + |o| (r_out + 16 u),      u = 2^-24
 
 * r_P: the weights are rounded to bf16 before the product with v in the bf16 mode (half a
-  step, 2^-8 relative), and a share of them is formed by a cubic that is off by at most
-  7.5e-5 relative, in the numerator and in the sum (twice); neither in fp32;
+  step, 2^-8 relative), and 7.5e-5 relative is left for the way they are formed, in the
+  numerator and in the sum (twice); neither in fp32;
 * e_s: a score is a sum of D products in fp32, each term and each partial sum rounded:
   |ds| <= (D + 3) u scale sum_d |q_d k_d|, which moves a weight by the factor e^ds, and the
   row's sum by no more: 2 e_s in all (the scores' products are exact: bf16 times bf16, or

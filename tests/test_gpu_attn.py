@@ -265,7 +265,7 @@ def test_prefill_growing_and_sharp_scores(dtype):
 
 
 def test_prefill_narrow_heads_growing_and_sharp_scores():
-    """The same at the other head width, whose steps form a share of the weights in another way."""
+    """The same at the other head width."""
     torch, G = _torch()
     g = _gen(13)
     T = 700
@@ -361,6 +361,38 @@ def test_prefill_nonfinite_in_masked_places(dtype, bad):
     o = _np(G.gdn_attn_prefill(q, k, v3))
     assert np.isfinite(o[0, :100]).all() and np.isfinite(o[0, :, 2:]).all()
     assert not np.isfinite(o[0, 100:, :2, 5]).any() and np.isfinite(np.delete(o[0], 5, axis=2)).all()
+    assert G.gdn_attn_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_prefill_nonfinite_keys_in_sight(dtype, bad, D):
+    """A key that is not finite, its value finite, at every place modulo 16 of a step that the later rows
+    see whole: NaN scores and scores of +inf make the rows that see them NaN, scores of -inf weigh nothing,
+    and the rows before are as if it were not there."""
+    torch, G = _torch()
+    g = _gen(20)
+    T, places, el = 400, range(16), 7
+    n = len(places)
+    q, k, v = (_draw(g, (1, T * n, h, D), dtype) for h in (2, 1, 1))
+    q[0, :, 0, el] = q[0, :, 0, el].abs() + 0.25        # head 0's score has the sign of `bad`,
+    q[0, :, 1, el] = -q[0, :, 1, el].abs() - 0.25       # head 1's the other
+    clean = k.clone()
+    at = [128 + 32 + p for p in places]
+    for i, a in enumerate(at):
+        k[0, i * T + a, 0, el] = bad
+    o = G.gdn_attn_prefill(q, k, v, cu_seqlens=_i32(_cu([T] * n)))
+    for i, a in enumerate(at):
+        s = slice(i * T, i * T + T)
+        kn, vn, oi = _np(clean[0, s]), _np(v[0, s]), o[0, s]
+        _check_rows(oi, q[0, s], kn, vn, 0, D ** -0.5, dtype, None, f"place {i}, before", [0, 127, 128, a - 1])
+        for h in (0, 1):
+            if np.isnan(bad) or (bad > 0) == (h == 0):
+                assert torch.isnan(oi[a:, h]).all(), f"place {i} head {h}"
+            else:
+                _check_rows(oi[1:, h:h + 1], q[0, s][1:, h:h + 1], np.delete(kn, a, 0), np.delete(vn, a, 0), 0, D ** -0.5,
+                            dtype, None, f"place {i} head {h}, behind", [a, 254, 255, 300, 382, 398])
     assert G.gdn_attn_status() == 0
 
 
