@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) attn_cc_join_kernel(AttnArgs a, Attn
         const float base = m == -INFINITY ? 0.f : m;
         for (int k = 0; k < n; ++k) {
             const float2 ml = p.ml[k * kM + row];
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;         // the row sees no key of this piece
+            // (a row that sees no key of the piece has m = -inf and zeros there)
             const float f = exp2f(ml.x - base);
             const float4 y = *reinterpret_cast<const float4*>(p.o + (int64_t)(k * kM + row) * D + c);
             l = fmaf(f, ml.y, l);

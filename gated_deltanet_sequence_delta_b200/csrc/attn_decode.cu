@@ -652,19 +652,18 @@ __global__ void __launch_bounds__(kThreads, 1) attn_decode_kernel(const __grid_c
                 float m = -INFINITY, l = 0.f;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                 for (int k = 0; k < 8; ++k) m = fmaxf(m, p[k * R * (D + 4) + D]);
+                const float base = m == -INFINITY ? 0.f : m;
                 for (int k = 0; k < 8; ++k) {
+                    // (a warp that took no key has m = -inf, l = 0, o = 0: it adds zeros; one whose keys all
+                    // score -inf may hold NaN, from values that are not finite, and hands them on)
                     const float* pk = p + k * R * (D + 4);
-                    // a warp that took no key: m = -inf, l = 0, o = 0
-                    const bool none = pk[D] == -INFINITY && pk[D + 1] == 0.f;
-                    const float f = none ? 0.f : exp2f(pk[D] - (m == -INFINITY ? 0.f : m));
+                    const float f = exp2f(pk[D] - base);
                     const float4 y = *reinterpret_cast<const float4*>(pk + c);
-                    if (f != 0.f || pk[D + 1] != 0.f) {
-                        l = fmaf(f, pk[D + 1], l);
-                        x.x = fmaf(f, y.x, x.x);
-                        x.y = fmaf(f, y.y, x.y);
-                        x.z = fmaf(f, y.z, x.z);
-                        x.w = fmaf(f, y.w, x.w);
-                    }
+                    l = fmaf(f, pk[D + 1], l);
+                    x.x = fmaf(f, y.x, x.x);
+                    x.y = fmaf(f, y.y, x.y);
+                    x.z = fmaf(f, y.z, x.z);
+                    x.w = fmaf(f, y.w, x.w);
                 }
                 if (whole) {
                     const bool none = P && past < 0 && past + r / G < 0;             // the row sees no key

@@ -659,9 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_prefill_kernel(const __grid_
                 ++outs;
             }
             if (it.slot >= 0) {
-                // a piece: the sums as they are, for the join
+                // a piece: the sums as they are, for the join (no sum where the second pass is to decide)
                 const int64_t pr = (int64_t)it.slot * kSplitRows + x * kRows + row;
-                if (live) plan.part_ml[pr] = make_float2(m, l);
+                if (live) plan.part_ml[pr] = make_float2(m, finite ? l : __int_as_float(0x7fffffff));
                 if (steps > 0) {
                     if (lane == 0) tc::mbar_arrive(&q_empty[x]);
                     // [4 columns][row]: a warp's rows lie together in every store

@@ -859,6 +859,42 @@ def test_two_graphs_share_a_workspace():
     assert G.gdn_attn_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("new,total", [(0, 17), (0, 3000), (1, 17), (4, 3000), (20, 2000), (200, 200)])
+def test_values_in_sight_behind_scores_of_minus_infinity(dtype, new, total):
+    """A key whose score is -inf weighs nothing, and 0 * inf is NaN: an infinite value there makes its column
+    NaN, whichever warp or block has only such keys (0 new tokens: decode).  The other columns are as if
+    the keys were not there."""
+    torch, G = _torch()
+    g = _gen(69)
+    D, col = 64, 5
+    for a, b in ((16, 17), (64, 128), (512, 1536), (600, 601)):
+        if b > total:
+            continue
+        c = Cache([total], 1, D, 16, dtype, 70)
+        q = _draw(g, (max(new, 1), 2, D), dtype)
+        q[..., 9] = q[..., 9].abs() + 0.25
+        kn, vn = c.seq(0)
+        at = c.slots(0, a, b)
+        c.k.view(-1, 1, D)[at, :, 9] = -float("inf")
+        c.v.view(-1, 1, D)[at, :, col] = float("inf")
+        past = total - q.shape[0]
+        rows = sorted({0, 15, 16, 17, 127, 128, 150, new // 2, new - 1} & set(range(q.shape[0]))) if new else [0]
+        if new == 0:
+            o = G.gdn_attn_decode(q, c.k, c.v, c.table, c.lens)
+        else:
+            o = G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, _i32([0, new]))
+        for r in rows:
+            seen = np.delete(np.arange(past + r + 1), np.arange(a, min(b, past + r + 1))) if past + r >= a else np.arange(past + r + 1)
+            want, bound = R.attention(_np(q[r:r + 1]), kn[seen], vn[seen], len(seen) - 1, D ** -0.5, dtype)
+            got = o[r:r + 1].clone()
+            if past + r >= a:
+                assert torch.isnan(got[..., col]).all(), (a, b, r)
+                got[..., col] = torch.from_numpy(want[..., col]).to(got)
+            _close(got, want, bound, f"keys {a} to {b}, row {r}")
+    assert G.gdn_attn_status() == 0
+
+
 # ---- bad tables (checked by paged.cuh, whose arithmetic test_attn_ref.py checks) --------------
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_bad_tables_are_reported_and_stay_contained(dtype):
