@@ -895,6 +895,43 @@ def test_values_in_sight_behind_scores_of_minus_infinity(dtype, new, total):
     assert G.gdn_attn_status() == 0
 
 
+def test_a_captured_call_with_other_lengths_and_pages():
+    """A graph's calls read lengths and tables when they run: replayed as contexts grow, shrink and become
+    idle, with another order of the pages and with pages that two sequences share."""
+    torch, G = _torch()
+    g = _gen(73)
+    D, page = 128, 16
+    longest = [1500, 700, 90, 3000]
+    c = Cache(longest, 2, D, page, "bf16", 74)
+    new = [20, 1, 3, 9]
+    cu = _i32(_cu(new))
+    q, qd = _draw(g, (sum(new), 8, D), "bf16"), _draw(g, (4, 8, D), "bf16")
+    n = max(G.attn_prefill_workspace_bytes(sum(new), 4, 8, 2, D, 1), G.attn_decode_workspace_bytes(4, 8, 2, D, 1))
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    step = lambda: (G.gdn_attn_prefill_paged(q, c.k, c.v, c.table, c.lens, cu, workspace=ws),
+                    G.gdn_attn_decode(qd, c.k, c.v, c.table, c.lens, workspace=ws))
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        op, od = step()
+    for totals, rows in (([1500, 700, 90, 3000], [0, 1, 2, 3]), ([1, 0, 90, 17], [0, 1, 2, 3]),
+                         ([700, 690, 90, 2999], [1, 1, 2, 3]), ([33, 64, 65, 1024], [3, 0, 1, 3])):
+        c.totals = totals
+        c.lens.copy_(_i32(totals))
+        keep = c.table_np
+        c.table_np = keep[rows]
+        c.table.copy_(torch.from_numpy(c.table_np))
+        graph.replay()
+        _check_decode(c, qd, od, "bf16", None, D ** -0.5, f"lengths {totals}")
+        for i, n in enumerate(new):
+            kn, vn = c.seq(i) if totals[i] else (np.zeros((0, 2, D)),) * 2
+            r = slice(_cu(new)[i], _cu(new)[i + 1])
+            _check_rows(op[r], q[r], kn, vn, totals[i] - n, D ** -0.5, "bf16", None, f"lengths {totals}, sequence {i}")
+        c.table_np = keep
+    assert G.gdn_attn_status() == 0
+
+
 # ---- bad tables (checked by paged.cuh, whose arithmetic test_attn_ref.py checks) --------------
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_bad_tables_are_reported_and_stay_contained(dtype):
