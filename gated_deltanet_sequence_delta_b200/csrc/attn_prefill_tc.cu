@@ -35,9 +35,10 @@
 // to bf16 for the product (half a step, 2^-8 relative, each); their sum is taken before the rounding.
 //
 // Measured, bf16: one prompt of 32K tokens, 16 heads over 4 of 128: 3.4 ms in short runs (1.28 PFLOP/s,
-// 0.76 of the matrix rate), 3.9-4.05 ms in long ones, where the power limit holds the clock at 1.6 GHz
-// (0.78 of the sustained matrix rate); 75K packed tokens, gated: 3.6-3.8 ms, 3.9-4.15 in long runs; pieces
-// over contexts to 24K, gated: 1.6 ms (1.8); 18 to 40 tokens over 13K in pages of 16: 92 us.
+// 0.76 of the matrix rate), 3.8-4.0 ms in long ones, where the power limit holds the clock at 1.63 GHz
+// (0.79 of the sustained matrix rate); 75K packed tokens, gated: 3.4-3.8 ms, 3.8-4.0 in long runs; pieces
+// over contexts to 24K, gated: 1.6 ms (1.8); 18 to 40 tokens over 13K in pages of 16: 90-92 us.  16 heads
+// over 4 of 64: 8K tokens 224 us, 32K 2.86 ms.
 //
 // Masked weights are exact zeros, but 0 * v is not 0 where v is infinite or NaN.  Values past
 // the last key that any row of the block sees are cleared in shared memory, by each tile before its
