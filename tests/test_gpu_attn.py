@@ -364,6 +364,25 @@ def test_prefill_nonfinite_in_masked_places(dtype, bad):
     assert G.gdn_attn_status() == 0
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_prefill_narrow_heads_nonfinite_in_masked_places(bad):
+    """The rows' own future and the next sequence, at the other head width, with the edge at every place
+    modulo 16."""
+    torch, G = _torch()
+    g = _gen(15)
+    T = 400
+    q, k, v = _draw(g, (1, T, 4, 64), "bf16"), _draw(g, (1, T, 2, 64), "bf16"), _draw(g, (1, T, 2, 64), "bf16")
+    clean = G.gdn_attn_prefill(q, k, v)
+    for at in range(280, 296):
+        k2, v2 = k.clone(), v.clone()
+        k2[:, at:], v2[:, at:] = bad, bad
+        for cu in (None, _i32([0, at, T])):
+            o = G.gdn_attn_prefill(q, k2, v2, cu_seqlens=cu)
+            _check_rows(o[0, :at], q[0, :at], _np(k[0]), _np(v[0]), 0, 0.125, "bf16", None, f"before {at}", [0, 255, 256, at - 1])
+            assert torch.equal(o[:, :128], clean[:, :128])
+    assert G.gdn_attn_status() == 0
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
